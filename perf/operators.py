@@ -372,16 +372,15 @@ def _assign_plain(s, rows):
     grow, give = (want - held).clamp(min=0), (held - want).clamp(min=0)
     taken = grow.sum()
     j = torch.arange(table.shape[1], device="cuda")
-    # taken pages: unit after unit from the lowest of the topmost `taken` free ones
-    first = n_free - taken + (grow.cumsum(0) - grow)
-    new = (j >= held[:, None]) & (j < want[:, None])
-    at = torch.where(new, first[:, None] + j - held[:, None], 0)
+    # pages given back go on top of the stack, unit after unit
     leaving = (j >= want[:, None]) & (j < held[:, None])
-    to = torch.where(leaving, (n_free - taken + (give.cumsum(0) - give))[:, None] + j - want[:, None], free.numel())
-    gone = torch.cat((free, free[:1])).scatter(0, to.view(-1), table.view(-1))
-    table.copy_(torch.where(new, free[at], torch.where(leaving, -1, table)))
-    free.copy_(gone[:-1])
+    to = torch.where(leaving, (n_free + give.cumsum(0) - give)[:, None] + j - want[:, None], free.numel())
+    free.copy_(torch.cat((free, free[:1])).scatter(0, to.view(-1), table.view(-1))[:-1])
     n_free += give.sum() - taken
+    # the topmost `taken` ones are taken, the lowest of them first
+    new = (j >= held[:, None]) & (j < want[:, None])
+    at = torch.where(new, (n_free + grow.cumsum(0) - grow)[:, None] + j - held[:, None], 0)
+    table.copy_(torch.where(new, free[at], torch.where(leaving, -1, table)))
     held.copy_(want)
 
 
