@@ -103,6 +103,16 @@ cudaError_t score_pass(const kvs_cache_desc& d, const void* K, const void* V, co
                            score, w_b, st);
 }
 
+kvs_status check_pool(const kvs_page_pool* p) {
+  if (!p || !p->pages || !p->table || p->n_pages <= 0 || p->max_pages <= 0)
+    return KVS_ERR_INVALID_ARG;
+  if (!aligned(p->pages, 16) || !aligned(p->table, 4)) return KVS_ERR_INVALID_ARG;
+  // slots and a unit's rows are int32
+  if (p->n_pages > INT32_MAX / KVS_PAGE_ROWS || p->max_pages > INT32_MAX / KVS_PAGE_ROWS)
+    return KVS_ERR_INVALID_ARG;
+  return KVS_OK;
+}
+
 kvs_status check_ws(void* ws, size_t ws_bytes, size_t need) {
   if (!ws || !aligned(ws, kWsAlign)) return KVS_ERR_WORKSPACE;
   if (ws_bytes < need) return KVS_ERR_WORKSPACE;
@@ -145,6 +155,9 @@ size_t kvs_workspace_size(const kvs_cache_desc* desc, int32_t W, int32_t op) {
     case KVS_OP_PREFILL:
       if (W < 1) return 0;
       return prefill_layout(*desc, W).total;
+    case KVS_OP_PAGES:
+      if ((long long)desc->B * desc->H_kv > INT32_MAX) return 0;
+      return page_layout_ws(*desc).total;
     default:
       return 0;
   }
@@ -374,6 +387,119 @@ kvs_status kvs_decode_attn(const kvs_cache_desc* desc, const void* q, void* K, v
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return from_cuda(launch_decode(*desc, q, K, V, logn, len, k_new, v_new, out, Ly,
                                  static_cast<char*>(ws), st));
+}
+
+size_t kvs_page_bytes(int32_t d) { return d == 64 || d == 128 ? (size_t)36 * d + 128 : 0; }
+
+kvs_status kvs_page_assign(const kvs_page_pool* pool, int32_t units, const int32_t* rows,
+                           int32_t* held, int32_t* free_pages, int32_t* n_free,
+                           const int32_t* slot_begin, int32_t* slots, int32_t slot_stride,
+                           void* ws, size_t ws_bytes, kvs_stream_t stream) {
+  kvs_status s = check_pool(pool);
+  if (s != KVS_OK) return s;
+  if (units <= 0 || !rows || !held || !free_pages || !n_free || (slots && slot_stride <= 0))
+    return KVS_ERR_INVALID_ARG;
+  if (!aligned(rows, 4) || !aligned(held, 4) || !aligned(free_pages, 4) || !aligned(n_free, 4) ||
+      !aligned(slot_begin, 4) || !aligned(slots, 4))
+    return KVS_ERR_INVALID_ARG;
+  const size_t n = (size_t)units * sizeof(int32_t);
+  const Range in[] = {{(const char*)rows, n}, {(const char*)slot_begin, slot_begin ? n : 0}};
+  const Range outs[] = {{(const char*)held, n},
+                        {(const char*)pool->table, n * pool->max_pages},
+                        {(const char*)free_pages, (size_t)pool->n_pages * sizeof(int32_t)},
+                        {(const char*)n_free, sizeof(int32_t)},
+                        {(const char*)slots, slots ? n * slot_stride : 0}};
+  for (int i = 0; i < 5; ++i) {
+    for (int j = 0; j < 2; ++j)
+      if (overlap(outs[i], in[j])) return KVS_ERR_ALIAS;
+    for (int j = i + 1; j < 5; ++j)
+      if (overlap(outs[i], outs[j])) return KVS_ERR_ALIAS;
+  }
+  s = check_ws(ws, ws_bytes, page_assign_bytes(units));
+  if (s != KVS_OK) return s;
+  return from_cuda(launch_page_assign(*pool, units, rows, held, free_pages, n_free, slot_begin,
+                                      slots, slot_stride, static_cast<char*>(ws),
+                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Rows of a cache and a slot for each, as kvs_page_store and kvs_page_load take them.
+static kvs_status check_page_rows(const kvs_cache_desc* desc, const kvs_page_pool* pool,
+                                  const void* K, const void* V, const float* logn,
+                                  const int32_t* slots, void* ws, size_t ws_bytes, bool load) {
+  kvs_status s = check_desc(desc);
+  if (s != KVS_OK) return s;
+  s = check_pool(pool);
+  if (s != KVS_OK) return s;
+  if (!K || !V || !slots) return KVS_ERR_INVALID_ARG;
+  if (!aligned(K, 16) || !aligned(V, 16) || !aligned(logn, 4) || !aligned(slots, 4))
+    return KVS_ERR_INVALID_ARG;
+  const size_t rows = (size_t)desc->B * desc->H_kv * desc->T_cap;
+  const Range pages{(const char*)pool->pages, pool->n_pages * kvs_page_bytes(desc->d)};
+  const Range arr[] = {{(const char*)K, cache_bytes(desc, desc->T_cap)},
+                       {(const char*)V, cache_bytes(desc, desc->T_cap)},
+                       {(const char*)logn, logn ? rows * sizeof(float) : 0},
+                       {(const char*)slots, rows * sizeof(int32_t)}};
+  for (int i = 0; i < 4; ++i) {
+    if (overlap(pages, arr[i])) return KVS_ERR_ALIAS;
+    for (int j = i + 1; j < 4 && load; ++j)
+      if (overlap(arr[i], arr[j])) return KVS_ERR_ALIAS;
+  }
+  return check_ws(ws, ws_bytes, kWsAlign);
+}
+
+kvs_status kvs_page_store(const kvs_cache_desc* desc, const void* K, const void* V,
+                          const float* logn, const int32_t* slots, const kvs_page_pool* pool,
+                          void* ws, size_t ws_bytes, kvs_stream_t stream) {
+  const kvs_status s = check_page_rows(desc, pool, K, V, logn, slots, ws, ws_bytes, false);
+  if (s != KVS_OK) return s;
+  return from_cuda(launch_page_store(*desc, K, V, logn, slots, *pool, static_cast<char*>(ws),
+                                     reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
+                         const int32_t* slots, void* K, void* V, float* logn, void* ws,
+                         size_t ws_bytes, kvs_stream_t stream) {
+  const kvs_status s = check_page_rows(desc, pool, K, V, logn, slots, ws, ws_bytes, true);
+  if (s != KVS_OK) return s;
+  return from_cuda(launch_page_load(*desc, *pool, slots, K, V, logn, static_cast<char*>(ws),
+                                    reinterpret_cast<cudaStream_t>(stream)));
+}
+
+kvs_status kvs_page_decode_attn(const kvs_cache_desc* desc, const void* q,
+                                const kvs_page_pool* pool, int32_t* len, const void* k_new,
+                                const void* v_new, void* out, void* ws, size_t ws_bytes,
+                                kvs_stream_t stream) {
+  kvs_status s = check_desc(desc);
+  if (s != KVS_OK) return s;
+  s = check_pool(pool);
+  if (s != KVS_OK) return s;
+  if (!q || !len || !out || (k_new == nullptr) != (v_new == nullptr)) return KVS_ERR_INVALID_ARG;
+  const size_t eb = elem_bytes(desc);
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(len, 4) || !aligned(k_new, eb) ||
+      !aligned(v_new, eb))
+    return KVS_ERR_INVALID_ARG;
+  const size_t units = (size_t)desc->B * desc->H_kv;
+  if (units > INT32_MAX) return KVS_ERR_INVALID_ARG;
+  const size_t qbytes = (size_t)desc->B * desc->H_q * desc->d * eb, nbytes = units * desc->d * eb;
+  // what the call writes (the pages, the lengths and the output) must not overlap the rest
+  const Range outs[] = {{(const char*)out, qbytes},
+                        {(const char*)pool->pages, pool->n_pages * kvs_page_bytes(desc->d)},
+                        {(const char*)len, units * sizeof(int32_t)}};
+  const Range in[] = {{(const char*)q, qbytes},
+                      {(const char*)pool->table, units * pool->max_pages * sizeof(int32_t)},
+                      {(const char*)k_new, k_new ? nbytes : 0},
+                      {(const char*)v_new, v_new ? nbytes : 0}};
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < 4; ++j)
+      if (overlap(outs[i], in[j])) return KVS_ERR_ALIAS;
+    for (int j = i + 1; j < 3; ++j)
+      if (overlap(outs[i], outs[j])) return KVS_ERR_ALIAS;
+  }
+  s = check_ws(ws, ws_bytes, page_layout_ws(*desc).total);
+  if (s != KVS_OK) return s;
+  return from_cuda(launch_page_decode(*desc, q, *pool, len, k_new, v_new, out,
+                                      static_cast<char*>(ws),
+                                      reinterpret_cast<cudaStream_t>(stream)));
 }
 
 kvs_status kvs_stream_read(const void* buf, int64_t rows, int32_t d, int32_t ctas, void* ws,

@@ -233,6 +233,35 @@ inline DecodeLayout decode_layout(const kvs_cache_desc& d) {
   return L;
 }
 
+// The 4-bit paged cache. The decode's work split gives every CTA of one wave (two per SM) an
+// equal run of pages, so a CTA leaves at most two partial rows per query head: one of a unit
+// that began before it, one of a unit that goes on after it. `done` counts the CTAs that are
+// through with the lengths (inside the flag word's block).
+constexpr int kPageDecodeCtas = kTargetCtas;
+struct PageLayoutWs {
+  size_t done, counters, part, total;
+};
+
+inline size_t page_persistent_bytes(int units) {
+  return kWsAlign + align_up((size_t)units * sizeof(int32_t), kWsAlign);
+}
+// scratch of the page table update: two offsets per unit, after the persistent region
+inline size_t page_assign_bytes(int units) {
+  return page_persistent_bytes(units) + align_up((size_t)units * 2 * sizeof(int32_t), kWsAlign);
+}
+
+inline PageLayoutWs page_layout_ws(const kvs_cache_desc& d) {
+  PageLayoutWs L;
+  const int units = d.B * d.H_kv;
+  L.done = kWsAlign / 2;
+  L.counters = kWsAlign;
+  L.part = page_persistent_bytes(units);
+  const size_t part = (size_t)kPageDecodeCtas * 2 * (d.H_q / d.H_kv) * (d.d + kPartPad) * sizeof(float);
+  L.total = align_up(L.part + part, kWsAlign);
+  if (L.total < page_assign_bytes(units)) L.total = page_assign_bytes(units);
+  return L;
+}
+
 // Chunked prefill: the score and merge scratch share one region (the score scratch is
 // dead once the pairs are scored), followed by the round's pair scores and weights and
 // the per-head candidate starts and targets.

@@ -1,0 +1,442 @@
+// GQA decode attention over the 4-bit paged cache (kvs_page_decode_attn).
+//
+// Attention of the KVSlimmer deep dive ("论文专题讲解：KVSlimmer：非对称 KV 合并的数学与工程",
+// §数学主线三) with the log-count bias of merged rows, over rows held in pages (pages.cuh):
+//   x_t = q . k_t / sqrt(d) + logn_t,  out = sum_t 2^(x_t log2 e - M) v_t / sum_t 2^(x_t log2 e - M)
+//
+// Work split. The pages of all units (KV heads of all sequences) are numbered one unit after
+// another, and CTA i takes pages [i c, (i + 1) c): lengths are ragged and known on the device
+// only, so every CTA sums them up for itself. A unit that lies in one CTA is finished there; one
+// that spans several gets a partial row per CTA in the workspace, and the last of them to arrive
+// (a counter per unit) combines. No CTA waits for another.
+//
+// A page is one contiguous block, so a single bulk copy (untiled, no tensor map) brings it into
+// the ring of the warp that works on it; each warp issues its own copies and needs no other
+// warp until the end of a unit.
+#include "decode_common.cuh"
+#include "kvs_common.cuh"
+#include "kvs_kernels.h"
+#include "pages.cuh"
+#include "ptx.cuh"
+
+namespace kvs {
+
+constexpr int kPdWarps = 8;
+constexpr int kPdThreads = kPdWarps * 32;
+constexpr int kPdStages = 2;
+
+template <int D, int G>
+struct PageDecodeShape {
+  static constexpr int kRing = kPdWarps * kPdStages * PageLayout<D>::kBytes;
+  static constexpr int kAcc = kPdWarps * G * D * 4;
+  static constexpr int kSmem = kRing + kAcc + kPdWarps * kPdStages * 8;
+  // the last CTA of a unit keeps its factors per query head and split where the warps' partial
+  // outputs were
+  static_assert(kPdWarps * D >= kPageDecodeCtas, "split factors");
+};
+
+// Weight of a partial (m, l, acc) against the reference M. One without a row that counts has
+// l = 0; NaN logits leave m at -inf and l NaN, which has to go through.
+__device__ __forceinline__ float part_weight(float m, float l, float M) {
+  return l != 0.f ? exp2f(m - M) : 0.f;
+}
+
+// Pages of a unit in the numbering: an empty one has one, so that a CTA finishes it.
+__device__ __forceinline__ int unit_span(int L) { return L > 0 ? pages_of(L) : 1; }
+
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPdThreads, 2)
+page_decode_kernel(const T* __restrict__ q, unsigned char* pages, const int32_t* __restrict__ table,
+                   int n_pages, int max_pages, int32_t* len, const T* __restrict__ k_new,
+                   const T* __restrict__ v_new, T* __restrict__ out, int units, int32_t* counters,
+                   int32_t* done, float* part, int32_t* flags) {
+  using P = PageLayout<D>;
+  using S = PageDecodeShape<D, G>;
+  constexpr int NW = kPdWarps, ST = kPdStages, RS = D + kPartPad;
+  extern __shared__ __align__(128) unsigned char dsm[];
+  unsigned char* ring = dsm + (threadIdx.x / 32) * ST * P::kBytes;          // this warp's stages
+  float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
+  uint64_t* full = reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc) + (threadIdx.x / 32) * ST;
+  __shared__ __align__(16) float qs[G][D];
+  __shared__ float s_m[NW][G], s_l[NW][G], s_new[G], s_stat[G][2];
+  __shared__ long long s_sum[NW];
+  __shared__ int s_unit, s_last;
+  __shared__ long long s_at;
+
+  griddep_wait();                 // launched with programmatic stream serialisation
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool want_append = k_new != nullptr;
+  const long long cap = (long long)max_pages * kPageRows;
+  auto length = [&](int u) {
+    const int L = len[u];
+    return L < 0 || L > cap ? 0 : L;
+  };
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+
+  // the numbering: total pages, and the unit and page this CTA starts with
+  const int per = (units + kPdThreads - 1) / kPdThreads;
+  const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
+  long long mine = 0;
+  for (int u = u0; u < u1; ++u) {
+    const int L = len[u];
+    if ((L < 0 || L > cap) && blockIdx.x == 0) set_flag(flags, KVS_FLAG_BAD_LENGTH);
+    mine += unit_span(length(u));
+  }
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) s_sum[warp] = inc;
+  __syncthreads();
+  long long total = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < warp) before += s_sum[w];
+    total += s_sum[w];
+  }
+  // at least one page per warp of a CTA: short caches gain nothing from more partial rows
+  long long chunk = (total + gridDim.x - 1) / gridDim.x;
+  if (chunk < NW) chunk = NW;
+  const long long f0 = blockIdx.x * chunk, f1 = min(total, f0 + chunk);
+  if (f0 < f1) {
+    long long at = before + inc - mine;
+    if (at <= f0 && f0 < at + mine) {
+      int u = u0;
+      for (; at + unit_span(length(u)) <= f0; ++u) at += unit_span(length(u));
+      s_unit = u;
+      s_at = at;
+    }
+  }
+  __syncthreads();
+
+  if (f0 < f1) {
+    // This warp's pages are f0 + warp, f0 + warp + NW, ... The issuing side runs ST pages ahead
+    // of the consuming side, each with its own place in the numbering.
+    struct Place {
+      int u, L;
+      long long at, end;           // the unit's pages are [at, end)
+    };
+    auto move_to = [&](Place& p, long long f) {
+      while (f >= p.end) {
+        ++p.u;
+        p.L = length(p.u);
+        p.at = p.end;
+        p.end = p.at + unit_span(p.L);
+      }
+    };
+    Place ip{s_unit, length(s_unit), s_at, 0};
+    ip.end = ip.at + unit_span(ip.L);
+    long long fi = f0 + warp;      // next page to issue
+    uint32_t loaded = 0;           // bit s: stage s holds (or is getting) a page
+    auto issue = [&](int s) {
+      loaded &= ~(1u << s);
+      if (fi < f1) {
+        move_to(ip, fi);
+        const long long j = fi - ip.at;
+        if (j * kPageRows < ip.L) {
+          const int id = table[(size_t)ip.u * max_pages + j];
+          if (id >= 0 && id < n_pages) {
+            loaded |= 1u << s;
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&full[s], P::kBytes);
+              bulk_load(ring + s * P::kBytes, pages + (size_t)id * P::kBytes, P::kBytes, &full[s]);
+            }
+          } else if (lane == 0) {
+            set_flag(flags, KVS_FLAG_BAD_PAGE);
+          }
+        }
+      }
+      fi += NW;
+    };
+    for (int s = 0; s < ST; ++s) issue(s);
+
+    const float qscale = kLog2e / sqrtf((float)D);
+    Place cp{s_unit, length(s_unit), s_at, 0};
+    cp.end = cp.at + unit_span(cp.L);
+    long long fc = f0 + warp;      // next page to consume
+    int stage = 0;
+    uint32_t phase = 0;            // bit s: parity of stage s
+    for (long long seg = f0; seg < f1;) {
+      move_to(cp, seg);
+      const int u = cp.u, L = cp.L;
+      const long long seg_end = min(f1, cp.end);
+      for (int i = tid; i < G * D; i += kPdThreads)
+        qs[i / D][i % D] = to_f32(q[(size_t)u * G * D + i]) * qscale;
+      __syncthreads();
+
+      constexpr int QL = D / 4, RPS = 32 / QL;       // lanes per row of V, rows at a time
+      float m[G], l[G], acc[G][4];
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        m[g] = -INFINITY;
+        l[g] = acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+      }
+      for (; fc < seg_end; fc += NW) {
+        const int nval = (int)min((long long)kPageRows, L - (fc - cp.at) * kPageRows);
+        if (loaded >> stage & 1u) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase >> stage & 1u))) {
+            // give up: give every copy in flight one more bound, then take no further page
+            set_flag(flags, KVS_FLAG_TIMEOUT);
+            for (int s = 0; s < ST; ++s)
+              if (loaded >> s & 1u) mbar_wait(&full[s], phase >> s & 1u);
+            loaded = 0;
+            fi = f1;
+            continue;
+          }
+          phase ^= 1u << stage;
+          const unsigned char* pg = ring + stage * P::kBytes;
+          // logits: lane = row
+          float x[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) x[g] = 0.f;
+#pragma unroll
+          for (int b = 0; b < P::nb; ++b) {
+            const uint4 w4 = *reinterpret_cast<const uint4*>(pg + P::k_code(b, lane));
+            const float s = __half2float(*reinterpret_cast<const __half*>(pg + P::k_scale(b, lane)));
+            const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
+            float y[G];
+#pragma unroll
+            for (int g = 0; g < G; ++g) y[g] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float k[8];
+              dequantise8(w[i], 1.f, k);
+#pragma unroll
+              for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int c = 0; c < 8; ++c) y[g] = fmaf(qs[g][b * 32 + i * 8 + c], k[c], y[g]);
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) x[g] = fmaf(y[g], s, x[g]);
+          }
+          const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane)) * kLog2e;
+          float p[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float xg = lane < nval ? x[g] + ln : -INFINITY;
+            const float M = fmaxf(m[g], warp_max(xg));
+            const float base = M == -INFINITY ? 0.f : M;
+            const float f = exp2f(m[g] - base);
+            p[g] = exp2f(xg - base);
+            l[g] = fmaf(l[g], f, p[g]);
+            m[g] = M;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) acc[g][c] *= f;
+          }
+          // values: lane = channel quad of row r0 + lane / QL
+          const int quad = lane % QL, b = quad / 8;
+          for (int r0 = 0; r0 < nval; r0 += RPS) {
+            const int r = r0 + lane / QL;
+            const uint32_t w = *reinterpret_cast<const uint16_t*>(pg + P::v_piece(b, r, quad % 8));
+            float s = __half2float(*reinterpret_cast<const __half*>(pg + P::v_scale(b, r)));
+            if (r >= nval) s = 0.f;                  // whatever the rest of the page holds
+            float v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = (float)((int)(w >> (4 * c) & 15u) - 8) * s;
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              const float pr = __shfl_sync(0xffffffffu, p[g], r);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) acc[g][c] = fmaf(pr, v[c], acc[g][c]);
+            }
+          }
+          __syncwarp();
+        }
+        issue(stage);
+        stage = stage + 1 == ST ? 0 : stage + 1;
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        const float ls = warp_sum(l[g]);
+        if (lane == 0) {
+          s_m[warp][g] = m[g];
+          s_l[warp][g] = ls;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (RPS == 2) acc[g][c] += __shfl_xor_sync(0xffffffffu, acc[g][c], 16);
+        if (lane < QL)
+          *reinterpret_cast<float4*>(s_acc + (warp * G + g) * D + lane * 4) =
+              make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+      }
+
+      // ---- the end of the unit in this CTA ----
+      const long long lp = L / kPageRows;            // the page a new row goes to
+      int new_id = -1;
+      if (want_append && len[u] == L && lp < max_pages) new_id = table[(size_t)u * max_pages + lp];
+      const bool fits = new_id >= 0 && new_id < n_pages;
+      if (fits)
+        for (int g = warp; g < G; g += NW) {
+          float sp = 0.f;
+          for (int c = lane; c < D; c += 32) sp = fmaf(qs[g][c], to_f32(k_new[(size_t)u * D + c]), sp);
+          sp = warp_sum(sp);
+          if (lane == 0) s_new[g] = sp;
+        }
+      __syncthreads();
+      const long long first = cp.at / chunk, last = (cp.end - 1) / chunk;
+      const int nsplit = (int)(last - first) + 1;
+      bool finish = true;
+      if (nsplit > 1) {
+        // slot 1 of the CTA the unit begins in, slot 0 of the others
+        float* row0 = part + ((size_t)blockIdx.x * 2 + (blockIdx.x == first ? 1 : 0)) * G * RS;
+        for (int i = tid; i < G * D; i += kPdThreads) {
+          const int g = i / D, c = i % D;
+          float M = -INFINITY, A = 0.f, Ls = 0.f;
+          for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][g]);
+          for (int w = 0; w < NW; ++w) {
+            const float f = part_weight(s_m[w][g], s_l[w][g], M);
+            A = fmaf(s_acc[(w * G + g) * D + c], f, A);
+            Ls = fmaf(s_l[w][g], f, Ls);
+          }
+          row0[g * RS + c] = A;
+          if (c == 0) {
+            row0[g * RS + D] = M;
+            row0[g * RS + D + 1] = Ls;
+          }
+        }
+        __syncthreads();
+        if (tid == 0) s_last = atom_add_acq_rel_gpu(&counters[u], 1) == nsplit - 1;
+        __syncthreads();
+        finish = s_last != 0;
+      }
+      if (finish) {
+        // factors of the partials (warps of this CTA, or the splits) and the new row
+        float* fac = nsplit > 1 ? s_acc : nullptr;   // [G][nsplit]
+        auto row_of = [&](int s) {
+          return part + ((size_t)(first + s) * 2 + (s == 0 ? 1 : 0)) * G * RS;
+        };
+        const int np = nsplit > 1 ? nsplit : NW;
+        for (int g = warp; g < G; g += NW) {
+          const float sn = fits ? s_new[g] : -INFINITY;
+          float M = sn;
+          for (int s = lane; s < np; s += 32)
+            M = fmaxf(M, nsplit > 1 ? __ldcg(row_of(s) + g * RS + D) : s_m[s][g]);
+          M = warp_max(M);
+          float Ls = 0.f;
+          for (int s = lane; s < np; s += 32) {
+            const float ms = nsplit > 1 ? __ldcg(row_of(s) + g * RS + D) : s_m[s][g];
+            const float ls = nsplit > 1 ? __ldcg(row_of(s) + g * RS + D + 1) : s_l[s][g];
+            const float f = part_weight(ms, ls, M);
+            Ls = fmaf(ls, f, Ls);
+            if (fac) fac[g * nsplit + s] = f;
+          }
+          Ls = warp_sum(Ls);
+          if (sn > -INFINITY) Ls += exp2f(sn - M);
+          if (lane == 0) {
+            s_stat[g][0] = M;
+            s_stat[g][1] = Ls;
+          }
+        }
+        __syncthreads();
+        for (int i = tid; i < G * D; i += kPdThreads) {
+          const int g = i / D, c = i % D;
+          const float M = s_stat[g][0], Ls = s_stat[g][1];
+          float A = 0.f;
+          if (nsplit > 1) {
+            for (int s = 0; s < nsplit; ++s) A = fmaf(__ldcg(row_of(s) + g * RS + c), fac[g * nsplit + s], A);
+          } else {
+            for (int w = 0; w < NW; ++w)
+              A = fmaf(s_acc[(w * G + g) * D + c], part_weight(s_m[w][g], s_l[w][g], M), A);
+          }
+          if (fits) A = fmaf(to_f32(v_new[(size_t)u * D + c]), exp2f(s_new[g] - M), A);
+          store_out<T>(out + (size_t)u * G * D + i, Ls == 0.f ? 0.f : A / Ls);   // 0: nothing attended
+        }
+        if (want_append && len[u] == L) {
+          if (fits) {
+            if (warp < 2) {
+              // warp 0 the key, warp 1 the value: 8 channels a lane
+              const T* src = (warp == 0 ? k_new : v_new) + (size_t)u * D;
+              float x[8];
+#pragma unroll
+              for (int c = 0; c < 8; ++c) x[c] = lane < D / 8 ? to_f32(src[lane * 8 + c]) : 0.f;
+              uint32_t sb;
+              const uint32_t w = quantise_lane<T>(x, sb);
+              unsigned char* pg = pages + (size_t)new_id * P::kBytes;
+              const int r = L % kPageRows, b = lane / 4, sub = lane % 4;
+              if (lane < D / 8) {
+                if (warp == 0) {
+                  *reinterpret_cast<uint32_t*>(pg + P::k_code(b, r) + sub * 4) = w;
+                  if (sub == 0) *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, r)) = (uint16_t)sb;
+                  if (lane == 0) *reinterpret_cast<float*>(pg + P::logn(r)) = 0.f;
+                } else {
+                  *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, r, sub * 2)) = (uint16_t)w;
+                  *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, r, sub * 2 + 1)) = (uint16_t)(w >> 16);
+                  if (sub == 0) *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, r)) = (uint16_t)sb;
+                }
+              }
+            }
+          } else if (tid == 0) {
+            set_flag(flags, KVS_FLAG_OUT_CAPACITY);
+          }
+        }
+        if (tid == 0 && nsplit > 1) counters[u] = 0;
+      }
+      seg = seg_end;
+      __syncthreads();            // the shared arrays are free for the next unit
+    }
+  }
+  if (want_append) {
+    // every CTA reads every length: they move on once the last CTA is through
+    __syncthreads();
+    if (tid == 0) s_last = atom_add_acq_rel_gpu(done, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (s_last) {
+      for (int u = tid; u < units; u += kPdThreads) {
+        const int L = len[u];
+        if (L < 0 || L >= cap) continue;
+        const int id = table[(size_t)u * max_pages + L / kPageRows];
+        if (id >= 0 && id < n_pages) len[u] = L + 1;
+      }
+      if (tid == 0) *done = 0;
+    }
+  }
+}
+
+template <typename T, int D, int G>
+static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_page_pool& pool,
+                            int32_t* len, const void* k_new, const void* v_new, void* out,
+                            char* ws, cudaStream_t st) {
+  using S = PageDecodeShape<D, G>;
+  auto kfn = page_decode_kernel<T, D, G>;
+  if (!ensure_smem_attr((const void*)kfn, S::kSmem)) return cudaErrorInvalidValue;
+  const int units = d.B * d.H_kv;
+  const PageLayoutWs Ly = page_layout_ws(d);
+  const cudaError_t e = launch_pdl(
+      kfn, dim3(kPageDecodeCtas), dim3(kPdThreads), S::kSmem, st, (const T*)q,
+      (unsigned char*)pool.pages, (const int32_t*)pool.table, pool.n_pages, pool.max_pages, len,
+      (const T*)k_new, (const T*)v_new, (T*)out, units, reinterpret_cast<int32_t*>(ws + Ly.counters),
+      reinterpret_cast<int32_t*>(ws + Ly.done), reinterpret_cast<float*>(ws + Ly.part),
+      reinterpret_cast<int32_t*>(ws));
+  count_launches(1);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_page_decode(const kvs_cache_desc& d, const void* q, const kvs_page_pool& pool,
+                               int32_t* len, const void* k_new, const void* v_new, void* out,
+                               char* ws, cudaStream_t st) {
+  const int G = d.H_q / d.H_kv;
+#define KVS_PD(TT, DD, GG) return launch_t<TT, DD, GG>(d, q, pool, len, k_new, v_new, out, ws, st)
+#define KVS_PD_G(TT, DD)        \
+  if (G == 1) KVS_PD(TT, DD, 1); \
+  if (G == 2) KVS_PD(TT, DD, 2); \
+  if (G == 4) KVS_PD(TT, DD, 4); \
+  if (G == 8) KVS_PD(TT, DD, 8)
+  if (d.dtype == KVS_BF16) {
+    if (d.d == 128) { KVS_PD_G(bf16, 128); }
+    else { KVS_PD_G(bf16, 64); }
+  } else {
+    if (d.d == 128) { KVS_PD_G(float, 128); }
+    else { KVS_PD_G(float, 64); }
+  }
+#undef KVS_PD_G
+#undef KVS_PD
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kvs

@@ -1,0 +1,126 @@
+// The 4-bit paged cache: page layout and the quantiser (include/kvs.h, kvs_page_pool).
+//
+// Every 32 channels of a row have one half-precision scale s, the smallest half >= max|x| / 7,
+// and 4-bit codes c + 8 with c = x / s rounded to the nearest integer, ties to even; the row
+// reads back as c s. s >= max|x| / 7 keeps c within [-7, 7] without a clamp, in the subnormal
+// halves too. A block that has no such s (a non-finite element, max|x| > 7 * 65504) gets a NaN
+// scale, so that it reads back as NaN.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "kvs_common.cuh"
+
+namespace kvs {
+
+constexpr int kPageRows = KVS_PAGE_ROWS;
+static_assert(kPageRows == 32, "one lane per row");
+
+// Byte offsets inside a page of D channels (nb = D / 32 scale blocks a row).
+//  K codes  [nb][32 rows][16 B]: the 32 channels of a block in order, low nibble first. Four
+//           lanes read a row's block as four words, and eight rows of it are 128 contiguous
+//           bytes: the A fragment of an m16n8k16 MMA without bank conflicts.
+//  V codes  [nb][16 row pairs][8 quads][2 rows][2 B]: the same two bytes of a channel quad, the
+//           rows of a pair side by side, so that one word holds a pair of consecutive rows (the
+//           MMA's k index) of four channels; each row still owns whole 16-bit pieces, so rows
+//           can be written one at a time.
+//  K scales [32 rows][nb] half: a lane takes all blocks of its row with one load.
+//  V scales [nb][32 rows] half: a lane takes a row pair of one block with one load.
+//  log-counts [32] fp32.
+template <int D>
+struct PageLayout {
+  static constexpr int nb = D / 32;
+  static constexpr int kK = 0;
+  static constexpr int kV = 16 * D;
+  static constexpr int kKs = 32 * D;
+  static constexpr int kVs = 34 * D;
+  static constexpr int kLn = 36 * D;
+  static constexpr int kBytes = 36 * D + 4 * kPageRows;
+  static_assert(kBytes % 16 == 0, "bulk copies");
+  // offsets of row r: the 16 B of K block b; the 16-bit V piece of quad `quad` of block b
+  __host__ __device__ static constexpr int k_code(int b, int r) { return kK + b * 512 + r * 16; }
+  __host__ __device__ static constexpr int v_piece(int b, int r, int quad) {
+    return kV + b * 512 + (r >> 1) * 32 + quad * 4 + (r & 1) * 2;
+  }
+  __host__ __device__ static constexpr int k_scale(int b, int r) { return kKs + (r * nb + b) * 2; }
+  __host__ __device__ static constexpr int v_scale(int b, int r) { return kVs + (b * kPageRows + r) * 2; }
+  __host__ __device__ static constexpr int logn(int r) { return kLn + r * 4; }
+};
+
+// Smallest half >= amax / 7, as bits; NaN when there is none. The nearest half of the product
+// with 1/7 is at most one step off; 7 h is exact in fp32 (3 + 11 bits), so the comparisons that
+// move it are too.
+__device__ __forceinline__ uint32_t scale_bits(float amax) {
+  if (!(amax <= 7.f * 65504.f)) return 0x7fffu;
+  uint32_t h = __half_as_ushort(__float2half_rn(amax * (1.f / 7.f)));
+  if (h > 0x7bffu) h = 0x7bffu;                      // rounded up to infinity: 65504 does
+  const float v = __half2float(__ushort_as_half((unsigned short)h));
+  if (7.f * v < amax) return h + 1;
+  if (h > 0) {
+    const float w = __half2float(__ushort_as_half((unsigned short)(h - 1)));
+    if (7.f * w >= amax) return h - 1;
+  }
+  return h;
+}
+
+// The 8 codes of x[0..7] as nibbles, low first, for the scale with bits `sb`.
+//
+// bf16 rows: x = m 2^e with m < 2^8, and a rounding border is (2k + 1) n 2^(f - 1) with
+// s = n 2^f, n < 2^11. Off a border, x is at least 2^(f - 1) or 2^e away from it, in units of s
+// at least 1 / 2n or 2^-8 x / s: more than 2^-12. x * (1/s) is off by at most 6.5 * 2^-24, so
+// adding 48 (last place 2^-18) puts a value on a border exactly back onto it and leaves the
+// others on their side; the second sum rounds to an integer, ties to even, and leaves c + 8 in
+// the low bits. fp32 rows: x and a border may be 2^-24 apart relative to each other, so the
+// quotient is rounded correctly by a division (a quotient off a border never rounds onto it: a
+// border has 4 bits).
+template <typename T>
+__device__ __forceinline__ uint32_t quantise8(const float* x, uint32_t sb) {
+  uint32_t w = 0;
+  const float s = __half2float(__ushort_as_half((unsigned short)sb));
+  if (sb == 0u || sb == 0x7fffu) return 0x88888888u;
+  if constexpr (sizeof(T) == 2) {
+    const float inv = __fdiv_rn(1.f, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float t = fmaf(x[i], inv, 48.f);
+      const uint32_t c = __float_as_uint(__fadd_rn(t, 12582912.f + 8.f - 48.f)) & 15u;
+      w |= c << (4 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = __float2int_rn(__fdiv_rn(x[i], s)) + 8;
+      w |= (uint32_t)c << (4 * i);
+    }
+  }
+  return w;
+}
+
+// Codes and scale of 8 channels of a row held by this lane, the 32 channels of a block being
+// held by four consecutive lanes (a multiple of 4 on). Whole warps take part.
+template <typename T>
+__device__ __forceinline__ uint32_t quantise_lane(const float* x, uint32_t& sb) {
+  float a = 0.f;
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a = fmaxf(a, fabsf(x[i]));
+    bad |= x[i] != x[i];                             // fmaxf drops a NaN
+  }
+  if (bad) a = INFINITY;
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  sb = scale_bits(a);
+  return quantise8<T>(x, sb);
+}
+
+// The 8 channels of a word of codes at scale s.
+__device__ __forceinline__ void dequantise8(uint32_t w, float s, float* x) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * s;
+}
+
+// Pages that `rows` rows fill; the decode counts an empty unit as one page.
+__host__ __device__ __forceinline__ int pages_of(int rows) { return (rows + kPageRows - 1) / kPageRows; }
+
+}  // namespace kvs

@@ -21,11 +21,13 @@ if not os.path.exists(_LIB_PATH):
 _lib = ctypes.CDLL(_LIB_PATH)
 
 F32, BF16 = 0, 1
-OP_SCORE, OP_MERGE, OP_DECODE, OP_PREFILL = 0, 1, 2, 3
+OP_SCORE, OP_MERGE, OP_DECODE, OP_PREFILL, OP_PAGES = 0, 1, 2, 3, 4
 SCOPE_HEAD, SCOPE_POOLED = 0, 1
+_DTYPES = {F32: torch.float32, BF16: torch.bfloat16}
 FORM_FULL, FORM_DIAGONAL, FORM_PER_QUERY = 0, 1, 2
 FLAG_BAD_LENGTH, FLAG_OUT_CAPACITY, FLAG_INPLACE_SPAN, FLAG_NONFINITE_STATS = 1, 2, 4, 8
-FLAG_TIMEOUT, FLAG_BUDGET = 16, 32
+FLAG_TIMEOUT, FLAG_BUDGET, FLAG_NO_PAGES, FLAG_BAD_PAGE = 16, 32, 64, 128
+PAGE_ROWS = 32
 
 STATUS = {0: "KVS_OK", 1: "KVS_ERR_INVALID_ARG", 2: "KVS_ERR_UNSUPPORTED", 3: "KVS_ERR_BUDGET",
           4: "KVS_ERR_WORKSPACE", 5: "KVS_ERR_ALIAS", 6: "KVS_ERR_CUDA"}
@@ -34,12 +36,18 @@ EXPORTS = ("kvs_workspace_size", "kvs_score_pairs", "kvs_merge_compact", "kvs_de
            "kvs_device_flags", "kvs_status_str", "kvs_version", "kvs_launch_count",
            "kvs_decode_attn_static", "kvs_static_scratch_bytes", "kvs_score_pairs_form",
            "kvs_prefill_chunk", "kvs_plan_rounds", "kvs_static_device_flags",
-           "kvs_stream_read")
+           "kvs_stream_read", "kvs_page_bytes", "kvs_page_assign", "kvs_page_store",
+           "kvs_page_load", "kvs_page_decode_attn")
 
 
 class CacheDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H_kv", ctypes.c_int32), ("H_q", ctypes.c_int32),
                 ("d", ctypes.c_int32), ("T_cap", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class PagePool(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32)]
 
 
 class KvsError(RuntimeError):
@@ -81,6 +89,17 @@ _lib.kvs_stream_read.restype = ctypes.c_int
 _lib.kvs_stream_read.argtypes = [_vp, ctypes.c_int64, _i32, _i32, _vp, _sz, _vp]
 _lib.kvs_static_device_flags.restype = ctypes.c_int
 _lib.kvs_static_device_flags.argtypes = [ctypes.POINTER(_i32), _i32, _vp]
+_PP = ctypes.POINTER(PagePool)
+_lib.kvs_page_bytes.restype = _sz
+_lib.kvs_page_bytes.argtypes = [_i32]
+_lib.kvs_page_assign.restype = ctypes.c_int
+_lib.kvs_page_assign.argtypes = [_PP, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _sz, _vp]
+_lib.kvs_page_store.restype = ctypes.c_int
+_lib.kvs_page_store.argtypes = [_P, _vp, _vp, _vp, _vp, _PP, _vp, _sz, _vp]
+_lib.kvs_page_load.restype = ctypes.c_int
+_lib.kvs_page_load.argtypes = [_P, _PP, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.kvs_page_decode_attn.restype = ctypes.c_int
+_lib.kvs_page_decode_attn.argtypes = [_P, _vp, _PP, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
 _lib.kvs_device_flags.argtypes = [_vp, ctypes.POINTER(_i32), _i32, _vp]
 
 if _lib.kvs_version() != 1:
@@ -240,3 +259,100 @@ def plan_rounds(length: int, target: int, cand_begin: int, n_recent: int, max_le
     _check(_lib.kvs_plan_rounds(int(length), int(target), int(cand_begin), int(n_recent), buf,
                                 int(max_lens), ctypes.byref(n)), "kvs_plan_rounds")
     return [int(buf[i]) for i in range(n.value + 1)]
+
+
+def page_bytes(d: int) -> int:
+    """Bytes of a page of 32 rows of d channels (0: head dim not built)."""
+    return int(_lib.kvs_page_bytes(int(d)))
+
+
+def page_pool(pages: torch.Tensor, table: torch.Tensor) -> PagePool:
+    """The pool of `pages` [n_pages, page_bytes(d)] (uint8) with the page tables `table`
+    [units, max_pages] (int32). It keeps both tensors alive."""
+    if pages.dim() != 2 or pages.dtype != torch.uint8 or pages.shape[1] not in (page_bytes(64), page_bytes(128)):
+        raise ValueError("pages must be uint8 [n_pages, page_bytes(d)]")
+    if table.dim() != 2 or table.dtype != torch.int32 or table.device != pages.device:
+        raise ValueError("table must be int32 [units, max_pages] on the pages' device")
+    pool = PagePool(_ptr(pages), _ptr(table), pages.shape[0], table.shape[1])
+    pool.tensors = (pages, table)
+    return pool
+
+
+def _page_args(pool: PagePool, ints, floats=(), dtype=None):
+    """Raw pointers of int32 tensors and of tensors of `dtype` that belong with `pool`: a
+    wrong type, device or layout would be read as something else, so it raises."""
+    dev = pool.tensors[0].device
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        raise ValueError(f"the pool is on {dev}, which is not the current device")
+    out = []
+    for tensors, want in ((ints, torch.int32), (floats, dtype)):
+        for t in tensors:
+            if t is None:
+                out.append(None)
+                continue
+            if t.dtype != want or t.device != dev or not t.is_contiguous():
+                raise ValueError(f"expected a contiguous {want} tensor on {dev}")
+            out.append(t.data_ptr())
+    return out
+
+
+def _page_shapes(desc: CacheDesc, pool: PagePool, units: int):
+    pages, table = pool.tensors
+    if pages.shape[1] != page_bytes(desc.d):
+        raise ValueError(f"the pool's pages are not pages of head dim {desc.d}")
+    if table.shape[0] < units:
+        raise ValueError(f"the pool has tables of {table.shape[0]} units, not {units}")
+
+
+def _sized(where: str, *pairs):
+    for t, n in pairs:
+        if t is not None and t.numel() != n:
+            raise ValueError(f"{where}: a tensor has {t.numel()} elements, not {n}")
+
+
+def page_assign(pool, rows, held, free_pages, n_free, ws, slots=None, slot_begin=None, stream=None):
+    """kvs_page_assign: every unit of rows [units] holds the pages of its rows; with slots
+    [units, stride], the slots of its rows from slot_begin on."""
+    units = rows.numel()
+    stride = 0 if slots is None else int(slots.shape[-1])
+    _sized("page_assign", (held, units), (free_pages, pool.n_pages), (n_free, 1), (slot_begin, units),
+           (slots, units * stride))
+    if pool.tensors[1].shape[0] < units:
+        raise ValueError(f"the pool has tables of {pool.tensors[1].shape[0]} units, not {units}")
+    a = _page_args(pool, (rows, held, free_pages, n_free, slot_begin, slots))
+    _check(_lib.kvs_page_assign(ctypes.byref(pool), units, *a, stride, _ptr(ws), ws.numel(),
+                                _stream(stream)), "kvs_page_assign")
+
+
+def page_store(desc, K, V, logn, slots, pool, ws, stream=None):
+    """kvs_page_store: the rows of K, V [B, H_kv, T_cap, d] into the pages at `slots`."""
+    rows = desc.B * desc.H_kv * desc.T_cap
+    _page_shapes(desc, pool, 0)
+    _sized("page_store", (K, rows * desc.d), (V, rows * desc.d), (logn, rows), (slots, rows))
+    s, k, v = _page_args(pool, (slots,), (K, V), _DTYPES[desc.dtype])
+    (ln,) = _page_args(pool, (), (logn,), torch.float32)
+    _check(_lib.kvs_page_store(ctypes.byref(desc), k, v, ln, s, ctypes.byref(pool), _ptr(ws),
+                               ws.numel(), _stream(stream)), "kvs_page_store")
+
+
+def page_load(desc, pool, slots, K, V, logn, ws, stream=None):
+    """kvs_page_load: the rows at `slots` back into K, V [B, H_kv, T_cap, d] and logn."""
+    rows = desc.B * desc.H_kv * desc.T_cap
+    _page_shapes(desc, pool, 0)
+    _sized("page_load", (K, rows * desc.d), (V, rows * desc.d), (logn, rows), (slots, rows))
+    s, k, v = _page_args(pool, (slots,), (K, V), _DTYPES[desc.dtype])
+    (ln,) = _page_args(pool, (), (logn,), torch.float32)
+    _check(_lib.kvs_page_load(ctypes.byref(desc), ctypes.byref(pool), s, k, v, ln, _ptr(ws),
+                              ws.numel(), _stream(stream)), "kvs_page_load")
+
+
+def page_decode_attn(desc, q, pool, lens, out, ws, k_new=None, v_new=None, stream=None):
+    """kvs_page_decode_attn: one decode step over the pages of every unit."""
+    units = desc.B * desc.H_kv
+    _page_shapes(desc, pool, units)
+    n = desc.B * desc.H_q * desc.d
+    _sized("page_decode_attn", (q, n), (out, n), (lens, units), (k_new, units * desc.d),
+           (v_new, units * desc.d))
+    ln, qp, op, kn, vn = _page_args(pool, (lens,), (q, out, k_new, v_new), _DTYPES[desc.dtype])
+    _check(_lib.kvs_page_decode_attn(ctypes.byref(desc), qp, ctypes.byref(pool), ln, kn, vn, op,
+                                     _ptr(ws), ws.numel(), _stream(stream)), "kvs_page_decode_attn")

@@ -71,7 +71,8 @@ typedef struct {
 
 typedef struct CUstream_st* kvs_stream_t; /* a cudaStream_t; NULL = legacy default stream */
 
-enum { KVS_OP_SCORE = 0, KVS_OP_MERGE = 1, KVS_OP_DECODE = 2, KVS_OP_PREFILL = 3 };
+enum { KVS_OP_SCORE = 0, KVS_OP_MERGE = 1, KVS_OP_DECODE = 2, KVS_OP_PREFILL = 3,
+       KVS_OP_PAGES = 4 };
 enum { KVS_SCOPE_HEAD = 0, KVS_SCOPE_POOLED = 1 };
 /* Scoring form: the coupled forward-only objective, or its diagonal-only ablation;
    either may be combined (bitwise or) with KVS_FORM_PER_QUERY, the per-query window
@@ -85,9 +86,12 @@ enum {
   KVS_FLAG_INPLACE_SPAN = 4,    /* in-place merge on a span longer than it supports; head skipped */
   KVS_FLAG_NONFINITE_STATS = 8, /* a window query had no finite softmax normaliser */
   KVS_FLAG_TIMEOUT = 16,        /* a pipeline wait gave up (bounded waits); results invalid */
-  KVS_FLAG_BUDGET = 32          /* a unit's target is below the shortest length repeated rounds
+  KVS_FLAG_BUDGET = 32,         /* a unit's target is below the shortest length repeated rounds
                                    can reach (every candidate span shrinks to one row at best);
                                    the unit still merges what it can this round */
+  KVS_FLAG_NO_PAGES = 64,       /* kvs_page_assign: the free pages do not cover the growth (or
+                                   the free stack is inconsistent); nothing was changed */
+  KVS_FLAG_BAD_PAGE = 128       /* a page number or slot outside the pool; those rows were skipped */
 };
 
 /*
@@ -318,6 +322,113 @@ size_t kvs_static_scratch_bytes(void);
  * `flags` receives the bits. Errors: KVS_ERR_INVALID_ARG (flags NULL), KVS_ERR_CUDA.
  */
 kvs_status kvs_static_device_flags(int32_t* flags, int32_t clear, kvs_stream_t stream);
+
+/*
+ * The 4-bit paged cache: a merged cache held in pages of 4-bit rows.
+ *
+ * A unit is one KV head of one sequence, u = b * H_kv + h. Its rows live in pages of
+ * KVS_PAGE_ROWS rows: page table[u][j] holds rows 32 j .. 32 j + 31. Units whose lengths
+ * differ (a pooled budget leaves every head its own) share one pool, and a row takes
+ * 9 d / 8 + 4 bytes: 148 instead of 516 at d = 128 in bf16.
+ *
+ * Format. For every 32 channels of a row: scale s = the smallest half-precision number
+ * >= max|x| / 7, codes c + 8 with c = x / s rounded to the nearest integer, ties to even
+ * (-7 <= c <= 7); the channels read back as c s. A block with a non-finite element, or
+ * with max|x| > 7 * 65504, has a NaN scale and reads back as NaN. With nb = d / 32 a page
+ * holds, one after the other (kvs_page_bytes(d) = 36 d + 128 bytes):
+ *   K codes    [nb][32 rows][16 B]  two channels a byte, the even one in the low nibble
+ *   V codes    [nb][16 row pairs][8 channel quads][2 rows][2 B]
+ *              the two bytes of channels 4 i .. 4 i + 3 of each row of the pair
+ *   K scales   [32 rows][nb] half
+ *   V scales   [nb][32 rows] half
+ *   log-counts [32] fp32
+ * Page contents of rows that no unit has may be anything.
+ */
+#define KVS_PAGE_ROWS 32
+
+/* A page pool and the page tables of the units that share it (host struct of device
+   pointers). n_pages and max_pages at most (2^31 - 1) / 32. */
+typedef struct {
+  void* pages;       /* [n_pages][kvs_page_bytes(d)], 16-byte aligned */
+  int32_t* table;    /* [units][max_pages] page numbers; -1 where a unit holds none */
+  int32_t n_pages;
+  int32_t max_pages; /* pages a unit can hold */
+} kvs_page_pool;
+
+/* Bytes of one page; 0 for a head dim that is not built (d in {64, 128}). */
+size_t kvs_page_bytes(int32_t d);
+
+/*
+ * kvs_page_assign -- page tables and slot maps from lengths, on the device.
+ *
+ * Afterwards unit u holds exactly ceil(rows[u] / 32) pages. First every unit that needs
+ * fewer gives back its last ones (a sequence that ends: rows 0), pushed on the free stack in
+ * (unit, page) order; then the T pages that other units need in all are taken off its top,
+ * the lowest of them first, in (unit, page) order. If the stack does not hold T pages,
+ * nothing changes and KVS_FLAG_NO_PAGES is set.
+ * A unit whose rows or held is out of range is left as it is (KVS_FLAG_BAD_LENGTH).
+ *
+ * Slot map (when slots is given): slots[u][i] = 32 * page + row of row slot_begin[u] + i of
+ * unit u for i < slot_stride, or -1 where that row is not below rows[u] or has no page.
+ * kvs_page_store and kvs_page_load take it.
+ *
+ * In:  pool (table updated; pages not touched), rows [units], slot_begin [units] (nullable:
+ *      0 everywhere).
+ * In/out: held [units] pages per unit (0 and table -1 at first), free_pages [n_pages],
+ *      n_free (one int32): the stack of free page numbers, free_pages[0 .. *n_free).
+ * Out: slots [units][slot_stride] (nullable).
+ * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes with B * H_kv >= units.
+ */
+kvs_status kvs_page_assign(const kvs_page_pool* pool, int32_t units, const int32_t* rows,
+                           int32_t* held, int32_t* free_pages, int32_t* n_free,
+                           const int32_t* slot_begin, int32_t* slots, int32_t slot_stride,
+                           void* ws, size_t ws_bytes, kvs_stream_t stream);
+
+/*
+ * kvs_page_store -- quantise rows of a cache into pages.
+ *
+ * Row t of unit u of K, V [B,H_kv,T_cap,d] and logn [B,H_kv,T_cap] (nullable: all counts 1)
+ * goes to slots[u][t] ([B,H_kv,T_cap]); a negative slot leaves the row out (it is not read),
+ * one past the pool sets KVS_FLAG_BAD_PAGE and is left out. Other rows of the pages stay as
+ * they are. No two rows may have the same slot (what that slot holds would be undefined).
+ * Workspace: at least 256 bytes (the flag word).
+ */
+kvs_status kvs_page_store(const kvs_cache_desc* desc, const void* K, const void* V,
+                          const float* logn, const int32_t* slots, const kvs_page_pool* pool,
+                          void* ws, size_t ws_bytes, kvs_stream_t stream);
+
+/*
+ * kvs_page_load -- read rows of pages back into a cache: the inverse of kvs_page_store
+ * (c s rounded to the cache's type). Rows with a negative slot are left as they are in K, V
+ * and logn (nullable); a slot past the pool sets KVS_FLAG_BAD_PAGE and is skipped.
+ * Workspace: at least 256 bytes (the flag word).
+ */
+kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
+                         const int32_t* slots, void* K, void* V, float* logn, void* ws,
+                         size_t ws_bytes, kvs_stream_t stream);
+
+/*
+ * kvs_page_decode_attn -- one decode step of GQA attention over the paged cache:
+ * kvs_decode_attn with the rows t < len[u] read from the pages.
+ *
+ * If k_new and v_new are given ([B, H_kv, d]), the row is attended as it is, written
+ * quantised to row len of every unit (count 1), and len is incremented. A unit without a
+ * page for that row sets KVS_FLAG_OUT_CAPACITY and is not changed (its output is written,
+ * without the new row): reserve the row with kvs_page_assign first. A unit with nothing to
+ * attend gets zeros. Rows whose page number is outside the pool are skipped
+ * (KVS_FLAG_BAD_PAGE). T_cap of desc is not used. Two units may share a page that neither
+ * appends to.
+ * In:  q [B,H_q,d]; pool; len [B*H_kv], 0 <= len <= 32 max_pages.
+ * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
+ * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes; its counters must be zero at
+ * the first call (each call leaves them zero). Make the first call for a device outside any
+ * stream capture (it sets a kernel attribute). Launched with programmatic stream
+ * serialisation, in plain stream order, as kvs_decode_attn is.
+ */
+kvs_status kvs_page_decode_attn(const kvs_cache_desc* desc, const void* q,
+                                const kvs_page_pool* pool, int32_t* len, const void* k_new,
+                                const void* v_new, void* out, void* ws, size_t ws_bytes,
+                                kvs_stream_t stream);
 
 /*
  * kvs_device_flags -- read (and optionally clear) the device flag word of a

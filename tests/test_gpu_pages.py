@@ -1,0 +1,623 @@
+"""The 4-bit paged cache on the GPU against the plain 64-bit checker in tests/pages_ref.py.
+
+Page tables, slot maps, page bytes and rows read back are exact. Decode outputs carry a bound
+that is derived, with A = sum_t p_t |v_t| and n rows:
+  fp32  d + 6 roundings of a logit's products and sums, each half a last place of at most
+        X = sum |q k| / sqrt(d) (+ |logn|), make the weights off by 2 (d + 6) 2^-24 X relative;
+        n + 16 roundings of the sums and the exponential's 2^-22 add to that.
+  bf16  in addition: the weight is rounded to half twice (alone, and times the row's scale),
+        2 * 2^-11, on the scale of A plus eight times the scale for the codes' offset; weights
+        below the half range are off by at most 2^-25 each, the largest being at least 2^6; and
+        the output is rounded to bf16, 2^-8 |out|.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import pages_ref as ref
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda")
+PAGE = 32
+
+
+@pytest.fixture(scope="module")
+def kvs():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from asymmetric_kv_merging_b200 import build
+    build.build()
+    from asymmetric_kv_merging_b200 import kvs as mod
+    return mod
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).to(DEV).contiguous()
+
+
+def workspace(kvs, B, H, G=1, d=64):
+    return kvs.workspace(kvs.make_desc(B, H, H * G, d, 2, kvs.BF16), ops=(kvs.OP_PAGES,))
+
+
+# ---------------------------------------------------------------------------
+# Page tables and slot maps
+# ---------------------------------------------------------------------------
+
+class DeviceTables:
+    def __init__(self, kvs, units, max_pages, free, n_pages=None):
+        self.kvs, n_pages = kvs, n_pages or len(free)
+        self.table = torch.full((units, max_pages), -1, dtype=torch.int32, device=DEV)
+        self.pages = torch.zeros(n_pages, kvs.page_bytes(64), dtype=torch.uint8, device=DEV)
+        self.pool = kvs.page_pool(self.pages, self.table)
+        self.held = torch.zeros(units, dtype=torch.int32, device=DEV)
+        self.free = i32(list(free) + [-7] * (n_pages - len(free)))
+        self.n_free = i32([len(free)])
+        self.ws = workspace(kvs, 1, units)
+
+    def assign(self, rows, slots=None, begin=None):
+        self.kvs.page_assign(self.pool, i32(rows), self.held, self.free, self.n_free, self.ws, slots,
+                             None if begin is None else i32(begin))
+
+    def check(self, want):
+        assert self.held.tolist() == want.held
+        assert np.array_equal(self.table.cpu().numpy(), want.table)
+        n = int(self.n_free)
+        assert self.free[:n].tolist() == want.free
+
+
+@pytest.mark.parametrize("units,max_pages", [(1, 1), (3, 5), (33, 9), (1025, 3), (5000, 2)])
+def test_tables_follow_random_lengths(kvs, units, max_pages):
+    rng = np.random.default_rng(units)
+    order = rng.permutation(units * max_pages)
+    dev, want = DeviceTables(kvs, units, max_pages, order), ref.Tables(units, max_pages, order.tolist())
+    for step in range(6):
+        rows = rng.integers(0, max_pages * PAGE + 1, units)
+        if step == 2:
+            rows[:] = 0                                     # everything goes back
+        begin = rng.integers(0, max_pages * PAGE, units) if step % 2 else np.zeros(units, int)
+        stride = [1, 7, 40][step % 3]
+        slots = torch.full((units, stride), -5, dtype=torch.int32, device=DEV)
+        dev.assign(rows, slots, begin if step % 2 else None)
+        assert want.assign(rows.tolist())
+        dev.check(want)
+        assert np.array_equal(slots.cpu().numpy(), want.slots(rows, begin, stride))
+    assert kvs.device_flags(dev.ws) == 0
+
+
+def test_one_unit_with_a_long_table(kvs):
+    order = list(range(4999, -1, -1))
+    dev, want = DeviceTables(kvs, 2, 5000, order), ref.Tables(2, 5000, order)
+    for rows in ([5000 * PAGE, 0], [31, 4998 * PAGE + 1], [0, 0]):
+        slots = torch.empty(2, 300, dtype=torch.int32, device=DEV)
+        dev.assign(rows, slots, [max(0, r - 300) for r in rows])
+        assert want.assign(rows)
+        dev.check(want)
+        assert np.array_equal(slots.cpu().numpy(), want.slots(rows, [max(0, r - 300) for r in rows], 300))
+
+
+def test_a_shortage_changes_nothing(kvs):
+    dev, want = DeviceTables(kvs, 3, 4, [5, 1, 4, 2], n_pages=6), ref.Tables(3, 4, [5, 1, 4, 2])
+    dev.assign([40, 0, 33])
+    assert want.assign([40, 0, 33])
+    dev.check(want)
+    slots = torch.empty(3, 70, dtype=torch.int32, device=DEV)
+    dev.assign([100, 40, 32], slots)       # four more pages wanted, one given back, none free
+    assert not want.assign([100, 40, 32])
+    dev.check(want)
+    assert np.array_equal(slots.cpu().numpy(), want.slots([100, 40, 32], [0, 0, 0], 70))
+    assert kvs.device_flags(dev.ws, clear=True) == kvs.FLAG_NO_PAGES
+    dev.assign([128, 0, 0])                # two more, and the two that are given back
+    assert want.assign([128, 0, 0])
+    dev.check(want)
+    dev.n_free.fill_(7)                    # more free pages than the pool has
+    dev.assign([0, 0, 0])
+    assert dev.held.tolist() == want.held and int(dev.n_free) == 7
+    assert kvs.device_flags(dev.ws, clear=True) == kvs.FLAG_NO_PAGES
+
+
+def test_lengths_out_of_range_leave_the_unit_alone(kvs):
+    dev, want = DeviceTables(kvs, 3, 4, range(12)), ref.Tables(3, 4, range(12))
+    for rows in ([50, 60, 70], [-1, 129, 10], [-2 ** 31, 2 ** 31 - 1, 128]):
+        slots = torch.empty(3, 4, dtype=torch.int32, device=DEV)
+        dev.assign(rows, slots)
+        assert want.assign(rows)
+        dev.check(want)
+        assert kvs.device_flags(dev.ws, clear=True) == (0 if rows[0] == 50 else kvs.FLAG_BAD_LENGTH)
+        if rows[0] < 0:
+            assert slots[0].tolist() == [-1] * 4
+
+
+# ---------------------------------------------------------------------------
+# Rows to pages and back
+# ---------------------------------------------------------------------------
+
+def hard_rows(rng, n, d, dtype):
+    """Rows with every kind of block: ordinary, on rounding borders, zero, tiny, huge, one large
+    element, infinite, NaN."""
+    x = rng.standard_normal((n, d))
+    x[n // 8] = 0
+    x[n // 8 + 1] *= 1e-7                                   # subnormal half scales
+    x[n // 8 + 2] *= 1e-9                                   # below the smallest scale's half step
+    x[n // 8 + 3] *= 6e4
+    x[n // 8 + 4, 1] = 1e4
+    for i in range(min(8, n - n // 8 - 5)):                 # multiples of half a scale: ties
+        half = 2.0 ** (i - 4)
+        x[n // 8 + 5 + i] = rng.integers(-14, 15, d) * half
+        x[n // 8 + 5 + i, ::32] = 14 * half
+    t = torch.tensor(x, dtype=torch.float32).to(dtype)
+    t[-1, 3], t[-2, 5], t[-3, d - 1] = float("inf"), float("nan"), 3e38
+    t[-4, 0] = 7 * 65504.0
+    return t
+
+
+def row_case(rng, B, H, T, d, dtype, shuffle):
+    n = B * H * T
+    K = torch.stack([hard_rows(rng, T, d, dtype) for _ in range(B * H)]).view(B, H, T, d)
+    V = torch.stack([hard_rows(rng, T, d, dtype).flip(0) for _ in range(B * H)]).view(B, H, T, d)
+    logn = torch.tensor(rng.standard_normal((B, H, T)), dtype=torch.float32)
+    n_pages = -(-n // PAGE) + 3
+    slots = np.arange(n) + PAGE
+    if shuffle:
+        slots = rng.permutation(n_pages * PAGE)[:n]
+    slots = np.where(rng.random(n) < 0.2, -rng.integers(1, 9, n), slots)
+    return K, V, logn, slots.reshape(B, H, T), n_pages
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shuffle", [False, True])
+@pytest.mark.parametrize("shape", [(1, 1, 24), (2, 3, 70)])
+def test_store_and_load_are_exact(kvs, dtype, d, shuffle, shape):
+    rng = np.random.default_rng(d + shuffle)
+    B, H, T = shape
+    K, V, logn, slots, n_pages = row_case(rng, B, H, T, d, dtype, shuffle)
+    before = rng.integers(0, 256, (n_pages, ref.page_bytes(d)), dtype=np.uint8)
+    pages = torch.tensor(before, device=DEV)
+    pool = kvs.page_pool(pages, torch.zeros(1, 1, dtype=torch.int32, device=DEV))
+    desc, ws = kvs.make_desc(B, H, H, d, T, dtype), workspace(kvs, B, H)
+    kvs.page_store(desc, K.to(DEV), V.to(DEV), logn.to(DEV), i32(slots), pool, ws)
+    want = before.copy()
+    Kn, Vn = K.double().numpy(), V.double().numpy()
+    for i in np.ndindex(B, H, T):
+        if slots[i] >= 0:
+            ref.put_row(want, slots[i], Kn[i], Vn[i], logn[i])
+    assert np.array_equal(pages.cpu().numpy(), want)        # rows left out, and other rows, as they were
+    # and back
+    Ko = torch.full_like(K, 77.0, device=DEV)
+    Vo, lo = torch.full_like(Ko, -77.0), torch.full((B, H, T), 5.0, device=DEV)
+    kvs.page_load(desc, pool, i32(slots), Ko, Vo, lo, ws)
+    live = slots >= 0
+    for got, x, fill in ((Ko, Kn, 77.0), (Vo, Vn, -77.0)):
+        back = torch.tensor(np.where(live[..., None], ref.held(x), fill)).to(torch.float32).to(dtype)
+        assert torch.equal(torch.nan_to_num(got.cpu(), nan=1e30), torch.nan_to_num(back, nan=1e30))
+    assert torch.equal(lo.cpu(), torch.where(torch.tensor(live), logn, torch.tensor(5.0)))
+    assert kvs.device_flags(ws) == 0
+
+
+def test_every_bf16_against_every_kind_of_scale(kvs):
+    """Blocks of all bf16 magnitudes below a maximum, for maxima of all mantissas: every code of
+    every scale, borders included."""
+    d = 64
+    bits = torch.arange(0x3f80 - 5 * 128, 0x3f80, dtype=torch.int16)
+    small = bits.view(torch.bfloat16)                       # 2^-5 .. 1
+    top = torch.arange(0x3f80, 0x3f80 + 128, dtype=torch.int16).view(torch.bfloat16)
+    rows = []
+    for m in top:
+        x = small.view(-1, 20)
+        rows.append(torch.cat([m.expand(x.shape[0], 1), x, -x[:, :11]], 1))
+    x = torch.cat(rows)
+    x = x[:x.shape[0] // 2 * 2].view(1, 1, -1, d).contiguous()
+    T = x.shape[2] // 2 * 2
+    x = x[:, :, :T].contiguous()
+    pages = torch.zeros(-(-T // PAGE), kvs.page_bytes(d), dtype=torch.uint8, device=DEV)
+    pool = kvs.page_pool(pages, torch.zeros(1, 1, dtype=torch.int32, device=DEV))
+    for dtype in (torch.bfloat16, torch.float32):
+        desc, ws = kvs.make_desc(1, 1, 1, d, T, dtype), workspace(kvs, 1, 1)
+        X, slots = x.to(dtype).to(DEV), i32(np.arange(T).reshape(1, 1, T))
+        kvs.page_store(desc, X, X, None, slots, pool, ws)
+        f32 = kvs.make_desc(1, 1, 1, d, T, torch.float32)
+        K, V = torch.empty(1, 1, T, d, device=DEV), torch.empty(1, 1, T, d, device=DEV)
+        kvs.page_load(f32, pool, slots, K, V, None, ws)
+        want = torch.tensor(ref.held(x.double().numpy())).float()
+        assert torch.equal(K.cpu(), want) and torch.equal(V.cpu(), want)
+
+
+def test_slots_past_the_pool_are_skipped(kvs):
+    d, T = 64, 4
+    pages = torch.zeros(2, kvs.page_bytes(d), dtype=torch.uint8, device=DEV)
+    pool = kvs.page_pool(pages, torch.zeros(1, 1, dtype=torch.int32, device=DEV))
+    desc, ws = kvs.make_desc(1, 1, 1, d, T, torch.bfloat16), workspace(kvs, 1, 1)
+    K = torch.ones(1, 1, T, d, dtype=torch.bfloat16, device=DEV)
+    slots = i32([[[64, 63, 2 ** 31 - 1, -1]]])
+    kvs.page_store(desc, K, K, None, slots, pool, ws)
+    assert kvs.device_flags(ws, clear=True) == kvs.FLAG_BAD_PAGE
+    Ko, Vo = torch.zeros_like(K), torch.zeros_like(K)
+    kvs.page_load(desc, pool, slots, Ko, Vo, None, ws)
+    assert kvs.device_flags(ws, clear=True) == kvs.FLAG_BAD_PAGE
+    assert torch.equal(Ko[0, 0, 1], K[0, 0, 1]) and float(Ko.float().abs().sum()) == d
+
+
+# ---------------------------------------------------------------------------
+# Decode attention
+# ---------------------------------------------------------------------------
+
+class Cache:
+    """A paged cache of given lengths with random pages; unused rows and pages hold garbage."""
+
+    def __init__(self, kvs, B, H, G, d, lens, dtype, seed=0, room=1, logn_scale=1.0, v_scale=1.0,
+                 k_scale=1.0):
+        self.kvs, self.B, self.H, self.G, self.d, self.dtype = kvs, B, H, G, d, dtype
+        rng = self.rng = np.random.default_rng(seed)
+        lens = self.lens_np = np.asarray(lens, np.int64)
+        units = B * H
+        held = -(-(lens + room) // PAGE)
+        maxp = int(held.max()) + 1
+        total = int(held.sum()) + 2
+        order = rng.permutation(total)
+        self.table_np = -np.ones((units, maxp), np.int64)
+        at = 0
+        for u in range(units):
+            self.table_np[u, :held[u]] = order[at:at + held[u]]
+            at += held[u]
+        self.pages_np = rng.integers(0, 256, (total, ref.page_bytes(d)), dtype=np.uint8)
+        self.pages_np[:, 32 * d:36 * d] = 255                # NaN scales where no row is
+        for u in range(units):
+            for t in range(lens[u]):
+                ref.put_row(self.pages_np, self.slot(u, t), rng.standard_normal(d) * k_scale,
+                            rng.standard_normal(d) * v_scale, rng.random() * logn_scale)
+        self.to_device()
+
+    def slot(self, u, t):
+        return int(self.table_np[u, t // PAGE]) * PAGE + t % PAGE
+
+    def to_device(self):
+        self.pages, self.table = torch.tensor(self.pages_np, device=DEV), i32(self.table_np)
+        self.lens = i32(self.lens_np)
+        self.pool = self.kvs.page_pool(self.pages, self.table)
+        self.desc = self.kvs.make_desc(self.B, self.H, self.H * self.G, self.d, 2, self.dtype)
+        self.ws = self.kvs.workspace(self.desc, ops=(self.kvs.OP_PAGES,))
+
+    def random(self, *shape, scale=1.0):
+        x = torch.tensor(self.rng.standard_normal(shape) * scale, dtype=torch.float32)
+        return x.to(self.dtype).to(DEV)
+
+    def step(self, q, k_new=None, v_new=None):
+        out = torch.full_like(q, 99.0)
+        self.kvs.page_decode_attn(self.desc, q, self.pool, self.lens, out, self.ws, k_new, v_new)
+        return out
+
+    def check(self, q, out, k_new=None, v_new=None, fits=None):
+        """`out` against attention over the rows as they were before the step."""
+        units, G, d = self.B * self.H, self.G, self.d
+        q, got = q.double().cpu().numpy().reshape(units, G, d), out.double().cpu().numpy().reshape(units, G, d)
+        worst = 0.0
+        for u in range(units):
+            k, v, ln = ref.rows_of(self.pages_np, self.table_np[u], int(self.lens_np[u]), d)
+            if k_new is not None and (fits is None or fits[u]):
+                k = np.concatenate([k, k_new.double().cpu().numpy().reshape(units, 1, d)[u]])
+                v = np.concatenate([v, v_new.double().cpu().numpy().reshape(units, 1, d)[u]])
+                ln = np.append(ln, 0.0)
+            want, size = ref.attend(q[u], k, v, ln)
+            bound = tolerance(self.dtype, q[u], k, v, ln, want, size)
+            err = np.abs(got[u] - want)
+            assert np.all(err <= bound), (u, len(k), float((err / bound).max()))
+            worst = max(worst, float((err / np.maximum(bound, 1e-300)).max()))
+        return worst
+
+    def append(self, k_new, v_new, fits=None):
+        """The step's effect on the checker's pages and lengths; the device's must be the same."""
+        for u in range(self.B * self.H):
+            if fits is None or fits[u]:
+                ref.put_row(self.pages_np, self.slot(u, int(self.lens_np[u])),
+                            k_new.double().cpu().numpy().reshape(-1, self.d)[u],
+                            v_new.double().cpu().numpy().reshape(-1, self.d)[u], 0.0)
+                self.lens_np[u] += 1
+        assert np.array_equal(self.pages.cpu().numpy(), self.pages_np)
+        assert self.lens.tolist() == self.lens_np.tolist()
+
+
+def tolerance(dtype, q, k, v, logn, want, size):
+    n, d = max(1, len(k)), q.shape[1]
+    if len(k) == 0:
+        return np.zeros_like(want)
+    x = float((np.abs(q) @ np.abs(k).T).max()) / np.sqrt(d) + float(np.abs(logn[np.isfinite(logn)]).max(initial=0.0))
+    rel = 2 * (d + 6) * 2.0 ** -24 * x + (n + 16) * 2.0 ** -24 + 2.0 ** -21
+    if dtype == torch.float32:
+        return rel * size + 2.0 ** -24 * np.abs(want) + 1e-30
+    scale = np.abs(v).max(0, keepdims=True) * 8 / 7 * 1.01         # eight times a row's scale at most
+    top = float(np.abs(v).max())
+    return (rel + 2 * 2.0 ** -11) * (size + scale) + n * 2.0 ** -27 * max(1.0, top) * (1 + top) + 2.0 ** -8 * np.abs(want)
+
+
+EDGE = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 255, 256, 257]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("G", [1, 2, 4, 8])
+def test_decode_at_the_edges_of_pages(kvs, dtype, d, G):
+    c = Cache(kvs, 2, 8, G, d, EDGE, dtype, seed=G + d)
+    q, kn, vn = c.random(2, 8 * G, d, scale=1.5), c.random(2, 8, d), c.random(2, 8, d)
+    c.check(q, c.step(q))
+    assert c.lens.tolist() == EDGE and np.array_equal(c.pages.cpu().numpy(), c.pages_np)
+    out = c.step(q, kn, vn)
+    c.check(q, out, kn, vn)
+    c.append(kn, vn)
+    c.check(q, c.step(q))
+    assert kvs.device_flags(c.ws) == 0
+
+
+@pytest.mark.parametrize("dtype,d,G,lens", [
+    (torch.bfloat16, 128, 4, [5000]),                        # one unit over many CTAs
+    (torch.float32, 128, 2, [3001]),
+    (torch.bfloat16, 64, 8, [2500, 3, 0, 1777]),
+    (torch.bfloat16, 128, 8, [1, 4097, 1, 31]),
+    (torch.float32, 64, 1, [900, 0, 901, 77])])
+def test_decode_of_long_and_ragged_units(kvs, dtype, d, G, lens):
+    c = Cache(kvs, 1, len(lens), G, d, lens, dtype, seed=3, logn_scale=3.0)
+    q = c.random(1, len(lens) * G, d, scale=2.0)
+    c.check(q, c.step(q))
+    kn, vn = c.random(1, len(lens), d), c.random(1, len(lens), d)
+    c.check(q, c.step(q, kn, vn), kn, vn)
+    c.append(kn, vn)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decode_of_many_short_units(kvs, dtype):
+    rng = np.random.default_rng(1)
+    lens = rng.integers(0, 40, 700)
+    lens[::50] = 0
+    c = Cache(kvs, 100, 7, 2, 64, lens, dtype, seed=2)
+    q, kn, vn = c.random(100, 14, 64), c.random(100, 7, 64), c.random(100, 7, 64)
+    c.check(q, c.step(q, kn, vn), kn, vn)
+    c.append(kn, vn)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decode_steps_cross_a_page(kvs, dtype):
+    c = Cache(kvs, 1, 4, 4, 128, [0, 30, 31, 61], dtype, seed=5, room=5)
+    for _ in range(5):
+        q, kn, vn = c.random(1, 16, 128), c.random(1, 4, 128), c.random(1, 4, 128)
+        c.check(q, c.step(q, kn, vn), kn, vn)
+        c.append(kn, vn)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("qs,ks,vs,ls", [(1, 1, 1e-4, 1), (1, 1, 1e-6, 1), (1, 1, 300., 1), (1, 1, 6e4, 1),
+                                         (1e-5, 1, 1, 1), (1e4, 1e-3, 1, 1), (8, 4, 1, 1), (1, 1e-6, 1, 1),
+                                         (1e-3, 2e3, 1, 40.)])
+def test_decode_over_the_range_of_values(kvs, dtype, qs, ks, vs, ls):
+    c = Cache(kvs, 1, 3, 4, 128, [300, 33, 1], dtype, seed=8, k_scale=ks, v_scale=vs, logn_scale=ls)
+    q = c.random(1, 12, 128, scale=qs)
+    q[0, 5] = 0
+    q[0, 6, 1:] = 0
+    c.check(q, c.step(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_decode_with_masked_rows(kvs, dtype):
+    """Log-counts of -inf or of the type's lowest value take rows out; a unit of nothing but
+    -inf is zeros; the lowest value everywhere is a uniform shift."""
+    c = Cache(kvs, 1, 4, 4, 64, [70, 40, 65, 64], dtype, seed=9)
+    low = float(np.finfo(np.float32).min)
+    for u, t, x in [(0, t, -np.inf) for t in range(0, 70, 3)] + [(1, t, -np.inf) for t in range(40)] + \
+            [(2, t, low / 2) for t in range(64)] + [(3, t, -np.inf) for t in range(32)]:
+        pg = c.pages_np[c.slot(u, t) // PAGE]
+        pg[36 * 64 + 4 * (t % PAGE):][:4] = np.frombuffer(np.float32(x).tobytes(), np.uint8)
+    c.to_device()
+    q = c.random(1, 16, 64)
+    out = c.step(q)
+    assert not out[0, 4:8].any()
+    got = out.double().cpu().numpy().reshape(4, 4, 64)
+    for u in (0, 2, 3):
+        k, v, ln = ref.rows_of(c.pages_np, c.table_np[u], int(c.lens_np[u]), 64)
+        keep = ln > low / 4
+        want, size = ref.attend(q.double().cpu().numpy().reshape(4, 4, 64)[u], k[keep], v[keep], ln[keep])
+        bound = tolerance(dtype, q.double().cpu().numpy().reshape(4, 4, 64)[u], k[keep], v[keep], ln[keep], want, size)
+        assert np.all(np.abs(got[u] - want) <= bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nan_stays_in_its_unit_or_query(kvs, dtype):
+    c = Cache(kvs, 1, 4, 2, 64, [50, 50, 50, 50], dtype, seed=10)
+    pg = c.pages_np[c.slot(1, 40) // PAGE]
+    pg[34 * 64 + (1 * 32 + 40 % PAGE) * 2:][:2] = 255                 # value block 1 of one row of unit 1
+    pg = c.pages_np[c.slot(3, 7) // PAGE]
+    pg[32 * 64 + (7 * 2 + 0) * 2:][:2] = 255                          # a key block of unit 3
+    c.to_device()
+    q = c.random(1, 8, 64)
+    q[0, 0, 9] = float("nan")                                         # query head 0 (unit 0)
+    out = c.step(q).float().cpu()
+    nan = torch.isnan(out[0])
+    assert nan[0].all() and not nan[1].any()
+    assert nan[2:4, 32:].all() and not nan[2:4, :32].any()
+    assert not nan[4:6].any() and nan[6:8].all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_full_units_and_bad_pages(kvs, dtype):
+    c = Cache(kvs, 1, 5, 2, 64, [64, 10, 32, 40, 40], dtype, seed=11, room=0)
+    c.table_np[0, 2:] = -1                                   # full: no page for row 64
+    c.table_np[2, 1:] = -1
+    c.table_np[4, 1] = len(c.pages_np)                       # past the pool: rows 32.. are skipped
+    c.lens_np[4] = 32                                        # what the checker sees of unit 4
+    c.to_device()
+    c.lens[4] = 40
+    q, kn, vn = c.random(1, 10, 64), c.random(1, 5, 64), c.random(1, 5, 64)
+    fits = [False, True, False, True, False]
+    c.check(q, c.step(q, kn, vn), kn, vn, fits)
+    assert kvs.device_flags(c.ws, clear=True) == kvs.FLAG_OUT_CAPACITY | kvs.FLAG_BAD_PAGE
+    assert c.lens.tolist() == [64, 11, 32, 41, 40]
+    # lengths out of range: zeros, and the length stays
+    c.lens.copy_(i32([-3, 11, 33 * PAGE, 41, 0]))
+    out = c.step(q, kn, vn)
+    assert not out[0, :2].any() and not out[0, 4:6].any() and out[0, 2:4].any()
+    assert kvs.device_flags(c.ws, clear=True) == kvs.FLAG_BAD_LENGTH
+    assert c.lens.tolist() == [-3, 12, 33 * PAGE, 42, 1]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_units_share_pages_that_none_appends_to(kvs, dtype):
+    c = Cache(kvs, 1, 2, 2, 128, [64, 70], dtype, seed=12)
+    c.table_np[0, :2] = c.table_np[1, :2]
+    c.to_device()
+    q, kn, vn = c.random(1, 4, 128), c.random(1, 2, 128), c.random(1, 2, 128)
+    c.check(q, c.step(q, kn, vn), kn, vn)
+    c.append(kn, vn)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_same_call_gives_the_same_bits(kvs, dtype):
+    c = Cache(kvs, 1, 3, 4, 128, [4000, 1, 333], dtype, seed=13)
+    q = c.random(1, 12, 128)
+    first = c.step(q)
+    for _ in range(20):
+        assert torch.equal(c.step(q), first)
+
+
+def test_captured_steps_replay_like_eager_ones(kvs):
+    eager = Cache(kvs, 1, 4, 4, 128, [500, 0, 31, 64], torch.bfloat16, seed=14, room=8)
+    graph = Cache(kvs, 1, 4, 4, 128, [500, 0, 31, 64], torch.bfloat16, seed=14, room=8)
+    q, kn, vn = eager.random(1, 16, 128), eager.random(1, 4, 128), eager.random(1, 4, 128)
+    lens0, pages0 = graph.lens.clone(), graph.pages.clone()
+    out = torch.empty_like(q)
+    call = lambda: kvs.page_decode_attn(graph.desc, q, graph.pool, graph.lens, out, graph.ws, kn, vn)   # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+        call()
+    graph.lens.copy_(lens0)
+    graph.pages.copy_(pages0)
+    for _ in range(3):
+        g.replay()
+        eager.step(q, kn, vn)
+        want = eager.step(q, kn, vn)
+        assert torch.equal(out, want) and torch.equal(graph.lens, eager.lens)
+        assert torch.equal(graph.pages, eager.pages)
+
+
+def test_two_streams_with_a_workspace_each(kvs):
+    a = Cache(kvs, 1, 4, 4, 128, [3000, 5, 70, 1000], torch.bfloat16, seed=15)
+    b = Cache(kvs, 2, 2, 4, 128, [10, 2900, 0, 64], torch.bfloat16, seed=16)
+    qa, qb = a.random(1, 16, 128), b.random(2, 8, 128)
+    want_a, want_b = a.step(qa), b.step(qb)
+    torch.cuda.synchronize()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    outs = []
+    for _ in range(30):
+        with torch.cuda.stream(sa):
+            outs.append((a.step(qa), want_a))
+        with torch.cuda.stream(sb):
+            outs.append((b.step(qb), want_b))
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in outs)
+
+
+def test_tensors_that_do_not_fit_are_refused(kvs):
+    c = Cache(kvs, 1, 2, 2, 64, [10, 20], torch.bfloat16, seed=17)
+    q, out = c.random(1, 4, 64), torch.empty(1, 4, 64, dtype=torch.bfloat16, device=DEV)
+    bad = [dict(q=q.float()), dict(q=q[:, :2]), dict(lens=c.lens.long()), dict(lens=c.lens.cpu()),
+           dict(out=torch.empty(1, 64, 4, dtype=torch.bfloat16, device=DEV).transpose(1, 2)),
+           dict(k_new=c.random(1, 2, 64).float()), dict(desc=kvs.make_desc(1, 2, 4, 128, 2, kvs.BF16)),
+           dict(desc=kvs.make_desc(1, 3, 6, 64, 2, kvs.BF16))]
+    for over in bad:
+        a = dict(desc=c.desc, q=q, pool=c.pool, lens=c.lens, out=out, ws=c.ws)
+        a.update(over)
+        with pytest.raises(ValueError):
+            kvs.page_decode_attn(**a)
+    for over, status in [(dict(k_new=c.random(1, 2, 64)), 1), (dict(out=q), 5), (dict(ws=c.ws[:256]), 4)]:
+        a = dict(desc=c.desc, q=q, pool=c.pool, lens=c.lens, out=out, ws=c.ws)
+        a.update(over)
+        with pytest.raises(kvs.KvsError) as e:
+            kvs.page_decode_attn(**a)
+        assert e.value.status == status
+
+
+# ---------------------------------------------------------------------------
+# As they are used together
+# ---------------------------------------------------------------------------
+
+def test_merge_store_decode_and_remerge(kvs):
+    """A merged cache goes into pages, decode appends to it, the newest segment is read back,
+    merged again in place and stored again, and decode goes on over the shorter cache."""
+    B, H, G, d, T, W = 2, 2, 4, 128, 512, 16
+    rng = np.random.default_rng(20)
+    bf = torch.bfloat16
+    rand = lambda *s: torch.tensor(rng.standard_normal(s), dtype=torch.float32).to(bf).to(DEV)    # noqa: E731
+    desc, units = kvs.make_desc(B, H, H * G, d, T, bf), B * H
+    ws = kvs.workspace(desc, W, ops=(kvs.OP_SCORE, kvs.OP_MERGE, kvs.OP_PAGES))
+    K, V, Q = rand(B, H, T, d), rand(B, H, T, d), rand(B, H * G, W, d)
+    logn, lens = torch.zeros(B, H, T, device=DEV), torch.full((units,), T, dtype=torch.int32, device=DEV)
+    cand = torch.full((units,), 8, dtype=torch.int32, device=DEV)
+    score, w_b = torch.zeros(B, H, T // 2, device=DEV), torch.zeros(B, H, T // 2, device=DEV)
+    Km, Vm, lm, nm = torch.zeros_like(K), torch.zeros_like(V), torch.zeros_like(logn), torch.zeros_like(lens)
+    kvs.score_pairs(desc, K, V, logn, lens, cand, W, Q, W, score, w_b, ws)
+    kvs.merge_compact(desc, K, V, logn, lens, cand, W, score, w_b,
+                      torch.full((B,), H * 300, dtype=torch.int32, device=DEV), kvs.SCOPE_POOLED, T, Km, Vm,
+                      lm, nm, ws)
+    rows = nm.tolist()                                       # pooled: every head has its own length
+    assert sum(rows) == B * H * 300
+
+    # into pages, with room for eight decoded rows
+    maxp, n_pages = T // PAGE, units * T // PAGE
+    pages = torch.full((n_pages, kvs.page_bytes(d)), 255, dtype=torch.uint8, device=DEV)
+    table = torch.full((units, maxp), -1, dtype=torch.int32, device=DEV)
+    pool = kvs.page_pool(pages, table)
+    held, n_free = torch.zeros(units, dtype=torch.int32, device=DEV), i32([n_pages])
+    free = i32(np.arange(n_pages))
+    slots = torch.empty(units, T, dtype=torch.int32, device=DEV)
+    kvs.page_assign(pool, nm, held, free, n_free, ws, slots)
+    kvs.page_store(desc, Km, Vm, lm, slots, pool, ws)
+    kvs.page_assign(pool, nm + 8, held, free, n_free, ws)
+    c = Cache.__new__(Cache)
+    c.kvs, c.B, c.H, c.G, c.d, c.dtype, c.rng = kvs, B, H, G, d, bf, rng
+    c.pages, c.table, c.pool, c.lens, c.ws, c.desc = pages, table, pool, nm, ws, desc
+
+    def decode(steps):
+        for _ in range(steps):
+            c.pages_np, c.table_np = pages.cpu().numpy(), table.cpu().numpy()
+            c.lens_np = np.array(nm.tolist())
+            q, kn, vn = rand(B, H * G, d), rand(B, H, d), rand(B, H, d)
+            c.check(q, c.step(q, kn, vn), kn, vn)
+            c.append(kn, vn)
+
+    decode(8)
+    # what the pages hold is the merged rows in 4 bits
+    for u in range(units):
+        k, v, ln = ref.rows_of(c.pages_np, c.table_np[u], rows[u], d)
+        at = (u // H, u % H)
+        assert np.array_equal(k, ref.held(Km[at][:rows[u]].double().cpu().numpy()))
+        assert np.array_equal(v, ref.held(Vm[at][:rows[u]].double().cpu().numpy()))
+        assert np.array_equal(ln, lm[at][:rows[u]].double().cpu().numpy())
+    # the newest 64 rows of every head: read back, merged to 32 in place, stored again
+    S = 64
+    start = nm - S
+    seg = torch.empty(units, S, dtype=torch.int32, device=DEV)
+    kvs.page_assign(pool, nm, held, free, n_free, ws, seg, start)
+    sdesc = kvs.make_desc(B, H, H * G, d, S, bf)
+    Ks, Vs, ls = torch.zeros(B, H, S, d, dtype=bf, device=DEV), torch.zeros(B, H, S, d, dtype=bf, device=DEV), \
+        torch.zeros(B, H, S, device=DEV)
+    kvs.page_load(sdesc, pool, seg, Ks, Vs, ls, ws)
+    sl = torch.full((units,), S, dtype=torch.int32, device=DEV)
+    zero = torch.zeros(units, dtype=torch.int32, device=DEV)
+    total = torch.exp(ls.double()).sum()
+    kvs.score_pairs(sdesc, Ks, Vs, ls, sl, zero, 0, Q, W, score, w_b, ws)
+    kvs.merge_compact(sdesc, Ks, Vs, ls, sl, zero, 0, score, w_b,
+                      torch.full((units,), 32, dtype=torch.int32, device=DEV), kvs.SCOPE_HEAD, S, Ks, Vs,
+                      ls, sl, ws)
+    assert sl.tolist() == [32] * units
+    assert torch.allclose(torch.exp(ls[:, :, :32].double()).sum(), total, rtol=1e-5)
+    nm.copy_(start + 32)
+    kvs.page_assign(pool, nm, held, free, n_free, ws, seg, start)
+    kvs.page_store(sdesc, Ks, Vs, ls, seg, pool, ws)
+    kvs.page_assign(pool, nm + 3, held, free, n_free, ws)
+    decode(3)
+    kvs.page_assign(pool, zero, held, free, n_free, ws)      # the batch ends: every page is free again
+    assert int(n_free) == n_pages and sorted(free.tolist()) == list(range(n_pages))
+    assert kvs.device_flags(ws) == 0
