@@ -28,11 +28,17 @@ constexpr int kPdStages = 2;
 template <int D, int G>
 struct PageDecodeShape {
   static constexpr int kRing = kPdWarps * kPdStages * PageLayout<D>::kBytes;
-  static constexpr int kAcc = kPdWarps * G * D * 4;
+  // the warps' partial outputs [NW][G][D]; the CTA that finishes a unit reuses them for the
+  // factors of the splits [G][CTAs] and the sums of all groups of threads but the first
+  static constexpr int kUnits = G * D / 4;                       // 4-column units of an output
+  static constexpr int kGroups = kPdThreads / kUnits;
+  static_assert(kUnits * kGroups == kPdThreads, "one thread per unit and group");
+  static constexpr int kFac = G * kPageDecodeCtas * 4;
+  static constexpr int kSums = (kGroups - 1) * kUnits * 16;
+  static constexpr int kPart = kPdWarps * G * D * 4;
+  static constexpr int kAcc = kPart > kFac + kSums ? kPart : kFac + kSums;
+  static_assert(kFac % 16 == 0 && kAcc % 16 == 0, "alignment");
   static constexpr int kSmem = kRing + kAcc + kPdWarps * kPdStages * 8;
-  // the last CTA of a unit keeps its factors per query head and split where the warps' partial
-  // outputs were
-  static_assert(kPdWarps * D >= kPageDecodeCtas, "split factors");
 };
 
 // Weight of a partial (m, l, acc) against the reference M. One without a row that counts has
@@ -395,6 +401,7 @@ page_decode_kernel(const T* __restrict__ q, unsigned char* pages, const int32_t*
   uint64_t* full = reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc) + (threadIdx.x / 32) * ST;
   __shared__ __align__(16) float qs[G][D];
   __shared__ float s_m[NW][G], s_l[NW][G], s_new[G], s_stat[G][2];
+  __shared__ float s_fac[G * NW];
   __shared__ long long s_sum[NW];
   __shared__ int s_unit, s_last;
   __shared__ long long s_at;
@@ -569,46 +576,113 @@ page_decode_kernel(const T* __restrict__ q, unsigned char* pages, const int32_t*
         finish = s_last != 0;
       }
       if (finish) {
-        // factors of the partials (warps of this CTA, or the splits) and the new row
-        float* fac = nsplit > 1 ? s_acc : nullptr;   // [G][nsplit]
+        // Sum the partials (the splits' rows in the workspace, or the warps' in shared memory):
+        // four columns a thread, the partials dealt out over NGRP threads for each four. The
+        // workspace rows are loaded in batches ahead of the factors, one round trip a batch.
+        constexpr int NU = S::kUnits, NGRP = S::kGroups;
+        constexpr int kBatch = 8;
+        const int grp = tid / NU, unit = tid % NU, g = unit * 4 / D, c = unit * 4 % D;
+        const int np = nsplit > 1 ? nsplit : NW;
         auto row_of = [&](int s) {
           return part + ((size_t)(first + s) * 2 + (s == 0 ? 1 : 0)) * G * RS;
         };
-        const int np = nsplit > 1 ? nsplit : NW;
-        for (int g = warp; g < G; g += NW) {
-          const float sn = fits ? s_new[g] : -INFINITY;
-          float M = sn;
-          for (int s = lane; s < np; s += 32)
-            M = fmaxf(M, nsplit > 1 ? __ldcg(row_of(s) + g * RS + D) : s_m[s][g]);
+        float4 v[kBatch];
+        if (nsplit > 1) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (grp + i * NGRP < np)
+              v[i] = __ldcg(reinterpret_cast<const float4*>(row_of(grp + i * NGRP) + g * RS + c));
+        }
+        float* fac = nsplit > 1 ? s_acc : s_fac;     // [G][np]
+        for (int gg = warp; gg < G; gg += NW) {
+          const float sn = fits ? s_new[gg] : -INFINITY;
+          constexpr int kMaxPer = (kPageDecodeCtas + 31) / 32;
+          float ms[kMaxPer], ls[kMaxPer], M = sn;
+#pragma unroll
+          for (int i = 0; i < kMaxPer; ++i) {
+            const int s = lane + i * 32;
+            ms[i] = -INFINITY;
+            ls[i] = 0.f;
+            if (s < np) {
+              if (nsplit > 1) {
+                const float2 ml = __ldcg(reinterpret_cast<const float2*>(row_of(s) + gg * RS + D));
+                ms[i] = ml.x;
+                ls[i] = ml.y;
+              } else {
+                ms[i] = s_m[s][gg];
+                ls[i] = s_l[s][gg];
+              }
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kMaxPer; ++i) M = fmaxf(M, ms[i]);
           M = warp_max(M);
           float Ls = 0.f;
-          for (int s = lane; s < np; s += 32) {
-            const float ms = nsplit > 1 ? __ldcg(row_of(s) + g * RS + D) : s_m[s][g];
-            const float ls = nsplit > 1 ? __ldcg(row_of(s) + g * RS + D + 1) : s_l[s][g];
-            const float f = part_weight(ms, ls, M);
-            Ls = fmaf(ls, f, Ls);
-            if (fac) fac[g * nsplit + s] = f;
+#pragma unroll
+          for (int i = 0; i < kMaxPer; ++i) {
+            const int s = lane + i * 32;
+            const float f = part_weight(ms[i], ls[i], M);
+            Ls = fmaf(ls[i], f, Ls);
+            if (s < np) fac[gg * np + s] = f;
           }
           Ls = warp_sum(Ls);
           if (sn > -INFINITY) Ls += exp2f(sn - M);
           if (lane == 0) {
-            s_stat[g][0] = M;
-            s_stat[g][1] = Ls;
+            s_stat[gg][0] = M;
+            s_stat[gg][1] = Ls;
           }
         }
         __syncthreads();
-        for (int i = tid; i < G * D; i += kPdThreads) {
-          const int g = i / D, c = i % D;
-          const float M = s_stat[g][0], Ls = s_stat[g][1];
-          float A = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = grp; s0 < np; s0 += kBatch * NGRP) {
           if (nsplit > 1) {
-            for (int s = 0; s < nsplit; ++s) A = fmaf(__ldcg(row_of(s) + g * RS + c), fac[g * nsplit + s], A);
+            if (s0 != grp) {
+#pragma unroll
+              for (int i = 0; i < kBatch; ++i)
+                if (s0 + i * NGRP < np)
+                  v[i] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + i * NGRP) + g * RS + c));
+            }
           } else {
-            for (int w = 0; w < NW; ++w)
-              A = fmaf(s_acc[(w * G + g) * D + c], part_weight(s_m[w][g], s_l[w][g], M), A);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+              if (s0 + i * NGRP < np)
+                v[i] = *reinterpret_cast<const float4*>(s_acc + ((s0 + i * NGRP) * G + g) * D + c);
           }
-          if (fits) A = fmaf(to_f32(v_new[(size_t)u * D + c]), exp2f(s_new[g] - M), A);
-          store_out<T>(out + (size_t)u * G * D + i, Ls == 0.f ? 0.f : A / Ls);   // 0: nothing attended
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (s0 + i * NGRP < np) {
+              const float f = fac[g * np + s0 + i * NGRP];
+              A.x = fmaf(v[i].x, f, A.x);
+              A.y = fmaf(v[i].y, f, A.y);
+              A.z = fmaf(v[i].z, f, A.z);
+              A.w = fmaf(v[i].w, f, A.w);
+            }
+        }
+        if constexpr (NGRP > 1) {
+          __syncthreads();                           // the warps' partials have been read
+          if (grp > 0) *reinterpret_cast<float4*>(s_acc + S::kFac / 4 + ((grp - 1) * NU + unit) * 4) = A;
+          __syncthreads();
+          if (grp == 0)
+#pragma unroll
+            for (int i = 0; i < NGRP - 1; ++i) {
+              const float4 w = *reinterpret_cast<const float4*>(s_acc + S::kFac / 4 + (i * NU + unit) * 4);
+              A.x += w.x; A.y += w.y; A.z += w.z; A.w += w.w;
+            }
+        }
+        if (grp == 0) {
+          const float M = s_stat[g][0], Ls = s_stat[g][1];
+          if (fits) {
+            const float f = exp2f(s_new[g] - M);
+            const T* vn = v_new + (size_t)u * D + c;
+            A.x = fmaf(to_f32(vn[0]), f, A.x); A.y = fmaf(to_f32(vn[1]), f, A.y);
+            A.z = fmaf(to_f32(vn[2]), f, A.z); A.w = fmaf(to_f32(vn[3]), f, A.w);
+          }
+          T* o = out + (size_t)u * G * D + unit * 4;
+          const bool none = Ls == 0.f;               // nothing attended: zeros
+          store_out<T>(o, none ? 0.f : A.x / Ls);
+          store_out<T>(o + 1, none ? 0.f : A.y / Ls);
+          store_out<T>(o + 2, none ? 0.f : A.z / Ls);
+          store_out<T>(o + 3, none ? 0.f : A.w / Ls);
         }
         if (want_append && len[u] == L) {
           if (fits) {
