@@ -137,10 +137,14 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# the handle of a device's current stream without building a Stream object (3 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _stream(stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        return _raw_stream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _check(status: int, where: str):
@@ -275,84 +279,84 @@ def page_pool(pages: torch.Tensor, table: torch.Tensor) -> PagePool:
         raise ValueError("table must be int32 [units, max_pages] on the pages' device")
     pool = PagePool(_ptr(pages), _ptr(table), pages.shape[0], table.shape[1])
     pool.tensors = (pages, table)
+    pool.device, pool.units = pages.get_device(), table.shape[0]
+    pool.head_dim = 64 if pages.shape[1] == page_bytes(64) else 128
     return pool
 
 
-def _page_args(pool: PagePool, ints, floats=(), dtype=None):
-    """Raw pointers of int32 tensors and of tensors of `dtype` that belong with `pool`: a
-    wrong type, device or layout would be read as something else, so it raises."""
-    dev = pool.tensors[0].device
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        raise ValueError(f"the pool is on {dev}, which is not the current device")
-    out = []
-    for tensors, want in ((ints, torch.int32), (floats, dtype)):
-        for t in tensors:
-            if t is None:
-                out.append(None)
-                continue
-            if t.dtype != want or t.device != dev or not t.is_contiguous():
-                raise ValueError(f"expected a contiguous {want} tensor on {dev}")
-            out.append(t.data_ptr())
-    return out
+def _arg(t: Optional[torch.Tensor], dtype, n: int, device: int):
+    """Raw pointer of a tensor that the library reads or writes as n elements of dtype; a wrong
+    type, size, device or layout would be read as something else, so it raises."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous {dtype} tensor of {n} elements on cuda:{device}, "
+                         f"not {t.dtype} of {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
-def _page_shapes(desc: CacheDesc, pool: PagePool, units: int):
-    pages, table = pool.tensors
-    if pages.shape[1] != page_bytes(desc.d):
-        raise ValueError(f"the pool's pages are not pages of head dim {desc.d}")
-    if table.shape[0] < units:
-        raise ValueError(f"the pool has tables of {table.shape[0]} units, not {units}")
+def _pool_device(pool: PagePool, units: int, d: Optional[int] = None) -> int:
+    """The device of a call on `pool`, which has to be the current one (kernels launch there)."""
+    device = pool.device
+    if device != torch.cuda.current_device():
+        raise ValueError(f"the pool is on {pool.tensors[0].device}, which is not the current device")
+    if pool.units < units:
+        raise ValueError(f"the pool has tables of {pool.units} units, not {units}")
+    if d is not None and d != pool.head_dim:
+        raise ValueError(f"the pool's pages are of head dim {pool.head_dim}, not {d}")
+    return device
 
 
-def _sized(where: str, *pairs):
-    for t, n in pairs:
-        if t is not None and t.numel() != n:
-            raise ValueError(f"{where}: a tensor has {t.numel()} elements, not {n}")
+def _page_stream(stream, device: int) -> int:
+    return _raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def page_assign(pool, rows, held, free_pages, n_free, ws, slots=None, slot_begin=None, stream=None):
     """kvs_page_assign: every unit of rows [units] holds the pages of its rows; with slots
     [units, stride], the slots of its rows from slot_begin on."""
     units = rows.numel()
-    stride = 0 if slots is None else int(slots.shape[-1])
-    _sized("page_assign", (held, units), (free_pages, pool.n_pages), (n_free, 1), (slot_begin, units),
-           (slots, units * stride))
-    if pool.tensors[1].shape[0] < units:
-        raise ValueError(f"the pool has tables of {pool.tensors[1].shape[0]} units, not {units}")
-    a = _page_args(pool, (rows, held, free_pages, n_free, slot_begin, slots))
-    _check(_lib.kvs_page_assign(ctypes.byref(pool), units, *a, stride, _ptr(ws), ws.numel(),
-                                _stream(stream)), "kvs_page_assign")
+    dev = _pool_device(pool, units)
+    stride = 0 if slots is None else slots.shape[-1]
+    i32 = torch.int32
+    _check(_lib.kvs_page_assign(
+        pool, units, _arg(rows, i32, units, dev), _arg(held, i32, units, dev),
+        _arg(free_pages, i32, pool.n_pages, dev), _arg(n_free, i32, 1, dev),
+        _arg(slot_begin, i32, units, dev), _arg(slots, i32, units * stride, dev), stride,
+        _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(), _page_stream(stream, dev)),
+        "kvs_page_assign")
 
 
 def page_store(desc, K, V, logn, slots, pool, ws, stream=None):
     """kvs_page_store: the rows of K, V [B, H_kv, T_cap, d] into the pages at `slots`."""
+    d, dtype = desc.d, _DTYPES[desc.dtype]
     rows = desc.B * desc.H_kv * desc.T_cap
-    _page_shapes(desc, pool, 0)
-    _sized("page_store", (K, rows * desc.d), (V, rows * desc.d), (logn, rows), (slots, rows))
-    s, k, v = _page_args(pool, (slots,), (K, V), _DTYPES[desc.dtype])
-    (ln,) = _page_args(pool, (), (logn,), torch.float32)
-    _check(_lib.kvs_page_store(ctypes.byref(desc), k, v, ln, s, ctypes.byref(pool), _ptr(ws),
-                               ws.numel(), _stream(stream)), "kvs_page_store")
+    dev = _pool_device(pool, 0, d)
+    _check(_lib.kvs_page_store(
+        desc, _arg(K, dtype, rows * d, dev), _arg(V, dtype, rows * d, dev),
+        _arg(logn, torch.float32, rows, dev), _arg(slots, torch.int32, rows, dev), pool,
+        _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(), _page_stream(stream, dev)),
+        "kvs_page_store")
 
 
 def page_load(desc, pool, slots, K, V, logn, ws, stream=None):
     """kvs_page_load: the rows at `slots` back into K, V [B, H_kv, T_cap, d] and logn."""
+    d, dtype = desc.d, _DTYPES[desc.dtype]
     rows = desc.B * desc.H_kv * desc.T_cap
-    _page_shapes(desc, pool, 0)
-    _sized("page_load", (K, rows * desc.d), (V, rows * desc.d), (logn, rows), (slots, rows))
-    s, k, v = _page_args(pool, (slots,), (K, V), _DTYPES[desc.dtype])
-    (ln,) = _page_args(pool, (), (logn,), torch.float32)
-    _check(_lib.kvs_page_load(ctypes.byref(desc), ctypes.byref(pool), s, k, v, ln, _ptr(ws),
-                              ws.numel(), _stream(stream)), "kvs_page_load")
+    dev = _pool_device(pool, 0, d)
+    _check(_lib.kvs_page_load(
+        desc, pool, _arg(slots, torch.int32, rows, dev), _arg(K, dtype, rows * d, dev),
+        _arg(V, dtype, rows * d, dev), _arg(logn, torch.float32, rows, dev),
+        _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(), _page_stream(stream, dev)),
+        "kvs_page_load")
 
 
 def page_decode_attn(desc, q, pool, lens, out, ws, k_new=None, v_new=None, stream=None):
     """kvs_page_decode_attn: one decode step over the pages of every unit."""
-    units = desc.B * desc.H_kv
-    _page_shapes(desc, pool, units)
-    n = desc.B * desc.H_q * desc.d
-    _sized("page_decode_attn", (q, n), (out, n), (lens, units), (k_new, units * desc.d),
-           (v_new, units * desc.d))
-    ln, qp, op, kn, vn = _page_args(pool, (lens,), (q, out, k_new, v_new), _DTYPES[desc.dtype])
-    _check(_lib.kvs_page_decode_attn(ctypes.byref(desc), qp, ctypes.byref(pool), ln, kn, vn, op,
-                                     _ptr(ws), ws.numel(), _stream(stream)), "kvs_page_decode_attn")
+    d, dtype, units = desc.d, _DTYPES[desc.dtype], desc.B * desc.H_kv
+    dev = _pool_device(pool, units, d)
+    n = desc.B * desc.H_q * d
+    _check(_lib.kvs_page_decode_attn(
+        desc, _arg(q, dtype, n, dev), pool, _arg(lens, torch.int32, units, dev),
+        _arg(k_new, dtype, units * d, dev), _arg(v_new, dtype, units * d, dev),
+        _arg(out, dtype, n, dev), _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(),
+        _page_stream(stream, dev)), "kvs_page_decode_attn")

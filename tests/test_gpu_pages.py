@@ -11,6 +11,8 @@ that is derived, with A = sum_t p_t |v_t| and n rows:
         the output is rounded to bf16, 2^-8 |out|.
 """
 
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -29,7 +31,9 @@ def kvs():
     from asymmetric_kv_merging_b200 import build
     build.build()
     from asymmetric_kv_merging_b200 import kvs as mod
-    return mod
+    yield mod
+    gc.collect()
+    torch.cuda.empty_cache()             # later tests watch the device's free memory
 
 
 def i32(x):
