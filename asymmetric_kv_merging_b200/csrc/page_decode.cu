@@ -13,6 +13,10 @@
 // A page is one contiguous block, so a single bulk copy (untiled, no tensor map) brings it into
 // the ring of the warp that works on it; each warp issues its own copies and needs no other
 // warp until the end of a unit.
+#include <map>
+#include <mutex>
+#include <utility>
+
 #include "decode_common.cuh"
 #include "kvs_common.cuh"
 #include "kvs_kernels.h"
@@ -44,14 +48,30 @@ struct PageDecodeShape {
 // Weight of a partial (m, l, acc) against the reference M. One without a row that counts has
 // l = 0; NaN logits leave m at -inf and l NaN, which has to go through.
 __device__ __forceinline__ float part_weight(float m, float l, float M) {
-  return l != 0.f ? exp2f(m - M) : 0.f;
+  return l != 0.f ? ex2_ftz(m - M) : 0.f;
 }
+
+constexpr int kPcWarps = 16;
+constexpr int kPcStages = 2;
+
+template <int D, int G>
+struct PageClusterShape {
+  static constexpr int kRing = kPcWarps * kPcStages * PageLayout<D>::kBytes;
+  static constexpr int kAcc = kPcWarps * G * D * 4;   // the warps' partial outputs
+  static constexpr int kSum = G * D * 4;              // their sum
+  static constexpr int kSmem = kRing + kAcc + kSum + kPcWarps * kPcStages * 8;
+};
+
+static bool use_cluster(int C, int max_pages) { return C >= 8 && max_pages <= 128 * C; }
 
 // Pages of a unit in the numbering: an empty one has one, so that a CTA finishes it.
 __device__ __forceinline__ int unit_span(int L) { return L > 0 ? pages_of(L) : 1; }
 
-// One warp's share of a unit: its softmax state over the pages it has taken. begin() loads the
-// unit's queries, take() adds the first nval rows of a page, end() writes the partial output
+__device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
+__device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
+
+// One warp's share of a unit: its softmax state over the pages it has taken. load() and begin()
+// take the unit's queries, take() adds the first nval rows of a page, end() writes the partial output
 // [G][D] and (m, l) per query head (log2 domain; m is a reference, not always the maximum).
 
 // fp32: CUDA cores, every product and sum in fp32. Logits with a lane per row, values with a lane
@@ -64,7 +84,8 @@ struct PageWarp {
   const float (*qs)[D];
   float m[G], l[G], acc[G][4];
 
-  __device__ __forceinline__ void begin(const T*, const float (*qs_)[D], int) {
+  __device__ __forceinline__ void load(const T*, int) {}
+  __device__ __forceinline__ void begin(const float (*qs_)[D], int) {
     qs = qs_;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -153,72 +174,100 @@ struct PageWarp {
 // The codes are never converted. A 4-bit code u in bits 0-3 or 4-7 of a 16-bit half IS the
 // subnormal half u 2^-24 or 16 u 2^-24, which the MMA multiplies exactly; so one AND makes an A
 // register out of a word of codes. The offset of 8 and the factors are put right outside:
-//   K: acc_b = sum_c u q' over a block of 32 channels, started at -8 2^-24 sum_c q' (so it ends as
-//      2^-24 sum c q'), then x += scale_b acc_b in fp32. q' is the query times a power of two that
-//      puts its largest element into [2^14, 2^15): exact in half, as are the 1/16 of the
-//      channels in bits 4-7, down to 2^-28 of the largest element.
+//   K: a_b = 2^-24 sum_c u q' over a block of 32 channels, x = sum_b scale_b (a_b - 8 2^-24 sum_c q').
+//      q' is the query times a power of two that puts its largest element into [2^14, 2^15): exact
+//      in half, as are the 1/16 of the channels in bits 4-7, down to 2^-28 of the largest
+//      element. The second sum is one more MMA: A is the rows' scales (their k slots repeated),
+//      B the blocks' sums of q' in three half parts (33 bits); it starts x.
 //   V: the block's scale goes onto the weights (B), w = half(half(p) scale), and
-//      sum_t (u - 8) w = sum_t u w - 8 sum_t w. The second sum is one more MMA per block whose A
-//      is 8 2^-24 in row b: all blocks share one accumulator. Both sums see the same rounded w,
-//      so the offset cancels to fp32 accuracy.
+//      sum_t (u - 8) scale p = sum_t u w - 8 sum_t scale p. The second sum is one MMA for all
+//      blocks, with the scales as A and the weights half(p) as B; it does not see the rounding
+//      of w, which therefore counts on |u| <= 15 instead of |u - 8| <= 7.
 // p and w are rounded to half (2^-11 each); the reference m keeps p scale <= 2^15 and the largest
 // p at 2^7 (over scales above 1) or more when it was set, so weights down to 2^-21 of the largest
 // stay normal halves, and below that the error is at most 2^-25 / 2^7 of it.
-// Instead of the 8 conversions and 8 products a word of codes would cost, it costs 5 integer
-// operations; per 16 rows x 128 channels about 190 instructions against the 2368 bytes read.
 template <int D, int G>
 struct PageWarp<bf16, D, G> {
   using P = PageLayout<D>;
   static constexpr int NB = P::nb;
+  uint4 raw[NB];               // the queries as loaded: lane (g, t) has channels 8 t.. of each block
   uint32_t qb[2 * NB][2];      // B of S^T: [2 b + i], k slots (8 t + 2 i, + 4) and (8 t + 2 i + 1, + 5)
-  float c0[NB], c1[NB];        // -8 2^-24 sum q' of block b for the heads 2 t and 2 t + 1
+  uint32_t cb[2];              // B of the offset: -8 2^-24 sum q' of the blocks, in three half parts
   float f0, f1;                // logit (log2) per unit of the scaled accumulators
   float m0, m1, l0, l1;
   float O[NB][2][4];           // rows: channels 4 g, 4 g + 1 | 4 g + 2, 4 g + 3 of block b
-  float off[4];                // row b: 8 2^-24 sum_t w of block b
+  float off[4];                // row b: sum_t p scale of block b
+  uint32_t poison;             // bit b: block b of some row reads as NaN
 
-  __device__ __forceinline__ void begin(const bf16* q, const float (*)[D], int lane) {
+  __device__ __forceinline__ void load(const bf16* q, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    uint4 raw[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      raw[b] = g < G ? *reinterpret_cast<const uint4*>(q + g * D + b * 32 + t * 8) : make_uint4(0, 0, 0, 0);
+  }
+
+  __device__ __forceinline__ void begin(const float (*)[D], int lane) {
+    const int t = lane & 3;
     uint32_t top = 0;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      raw[b] = g < G ? *reinterpret_cast<const uint4*>(q + g * D + b * 32 + t * 8) : make_uint4(0, 0, 0, 0);
+    for (int b = 0; b < NB; ++b)
       top = __vmaxu2(top, __vmaxu2(__vmaxu2(raw[b].x & 0x7fff7fffu, raw[b].y & 0x7fff7fffu),
                                    __vmaxu2(raw[b].z & 0x7fff7fffu, raw[b].w & 0x7fff7fffu)));
-    }
     top = max(top & 0xffffu, top >> 16);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int e = top == 0u ? 0 : max(-102, min(126, 14 + 127 - (int)(top >> 7)));
     const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     const float f = __uint_as_float((uint32_t)(127 + 24 - e) << 23) * (kLog2e / sqrtf((float)D));
+    uint32_t part[NB / 2][4];                        // of blocks 2 b and 2 b + 1; the fourth is 0
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float x[8] = {bf16_lo(raw[b].x), bf16_hi(raw[b].x), bf16_lo(raw[b].y), bf16_hi(raw[b].y),
-                    bf16_lo(raw[b].z), bf16_hi(raw[b].z), bf16_lo(raw[b].w), bf16_hi(raw[b].w)};
-      float sum = 0.f;
+    for (int b2 = 0; b2 < NB / 2; ++b2) {
+      float c[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float w = i & 1 ? up * 0.0625f : up;
-        const __half2 h = __floats2half2_rn(x[i] * w, x[i + 4] * w);
-        qb[2 * b + i / 2][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
-        const float2 back = __half22float2(h);
-        sum += (back.x + back.y) * (i & 1 ? 16.f : 1.f);
+      for (int k = 0; k < 2; ++k) {
+        const int b = 2 * b2 + k;
+        float x[8] = {bf16_lo(raw[b].x), bf16_hi(raw[b].x), bf16_lo(raw[b].y), bf16_hi(raw[b].y),
+                      bf16_lo(raw[b].z), bf16_hi(raw[b].z), bf16_lo(raw[b].w), bf16_hi(raw[b].w)};
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = i & 1 ? up * 0.0625f : up;
+          const __half2 h = __floats2half2_rn(x[i] * w, x[i + 4] * w);
+          qb[2 * b + i / 2][i & 1] = *reinterpret_cast<const uint32_t*>(&h);
+          const float2 back = __half22float2(h);
+          sum += (back.x + back.y) * (i & 1 ? 16.f : 1.f);
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        c[k] = sum * (-8.f / 16777216.f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) O[b][0][i] = O[b][1][i] = 0.f;
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      sum *= -8.f / 16777216.f;
-      c0[b] = __shfl_sync(0xffffffffu, sum, t * 8);
-      c1[b] = __shfl_sync(0xffffffffu, sum, t * 8 + 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) O[b][0][i] = O[b][1][i] = 0.f;
+      for (int i = 0; i < 3; ++i) {
+        const __half2 h = __floats2half2_rn(c[0], c[1]);
+        part[b2][i] = *reinterpret_cast<const uint32_t*>(&h);
+        const float2 back = __half22float2(h);
+        c[0] -= back.x;
+        c[1] -= back.y;
+      }
+      part[b2][3] = 0u;
+    }
+    // k slots: part after part, the blocks of a part in order
+    if constexpr (NB == 4) {
+      const uint32_t lo = t & 2 ? part[0][1] : part[0][0], hi = t & 2 ? part[1][1] : part[1][0];
+      cb[0] = t & 1 ? hi : lo;
+      cb[1] = t & 2 ? 0u : t & 1 ? part[1][2] : part[0][2];
+    } else {
+      cb[0] = t == 0 ? part[0][0] : t == 1 ? part[0][1] : t == 2 ? part[0][2] : 0u;
+      cb[1] = 0u;
     }
     f0 = __shfl_sync(0xffffffffu, f, t * 8);
     f1 = __shfl_sync(0xffffffffu, f, t * 8 + 4);
     m0 = m1 = -INFINITY;
     l0 = l1 = 0.f;
     off[0] = off[1] = off[2] = off[3] = 0.f;
+    poison = 0u;
   }
 
   __device__ __forceinline__ void take(unsigned char* pg, int nval, int lane) {
@@ -237,19 +286,25 @@ struct PageWarp<bf16, D, G> {
     for (int i = 0; i < 2; ++i) {
       const int r = i * 16 + g;
       __half2 sa[NB / 2], sb[NB / 2];            // K scales of rows r and r + 8
-#pragma unroll
-      for (int b = 0; b < NB / 2; ++b) {
-        sa[b] = *reinterpret_cast<const __half2*>(pg + P::k_scale(2 * b, r));
-        sb[b] = *reinterpret_cast<const __half2*>(pg + P::k_scale(2 * b, r + 8));
+      if constexpr (NB == 4) {
+        const uint2 u = *reinterpret_cast<const uint2*>(pg + P::k_scale(0, r));
+        const uint2 v = *reinterpret_cast<const uint2*>(pg + P::k_scale(0, r + 8));
+        sa[0] = as_half2(u.x); sa[1] = as_half2(u.y);
+        sb[0] = as_half2(v.x); sb[1] = as_half2(v.y);
+      } else {
+        sa[0] = *reinterpret_cast<const __half2*>(pg + P::k_scale(0, r));
+        sb[0] = *reinterpret_cast<const __half2*>(pg + P::k_scale(0, r + 8));
       }
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
+      const uint32_t za = as_u32(t & 1 ? sa[NB / 2 - 1] : sa[0]), zb = as_u32(t & 1 ? sb[NB / 2 - 1] : sb[0]);
+      float y[4];
+      mma_f16_16816(y, za, zb, za, zb, cb[0], cb[1], 0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const uint32_t wa = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, r) + t * 4);
         const uint32_t wb = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, r + 8) + t * 4);
         float a[4];
-        mma_f16_16816(a, wa & LO, wb & LO, wa & HI, wb & HI, qb[2 * b][0], qb[2 * b][1], c0[b],
-                      c1[b], c0[b], c1[b]);
+        mma_f16_16816(a, wa & LO, wb & LO, wa & HI, wb & HI, qb[2 * b][0], qb[2 * b][1], 0.f, 0.f,
+                      0.f, 0.f);
         const uint32_t ua = wa >> 8, ub = wb >> 8;
         mma_f16_16816(a, ua & LO, ub & LO, ua & HI, ub & HI, qb[2 * b + 1][0], qb[2 * b + 1][1],
                       a[0], a[1], a[2], a[3]);
@@ -281,7 +336,19 @@ struct PageWarp<bf16, D, G> {
     }
     smax = __reduce_max_sync(0xffffffffu, max(smax & 0xffffu, smax >> 16));
     const float ev = (float)max(0, (int)(smax >> 10) - 14);
-    const bool poison = smax > 0x7c00u;          // a block that reads as NaN
+    if (smax > 0x7c00u) {
+      // Blocks that read as NaN: 0 x NaN would reach the other blocks through the shared sum of
+      // weights, so the scales go and end() puts the NaN where it belongs.
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint16_t* sp = reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane));
+        const bool bad = *sp > 0x7c00u;
+        if (bad) *sp = 0;
+        if (__any_sync(0xffffffffu, bad)) poison |= 1u << b;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+    }
     // The reference of a column moves only when a weight would pass 2^15, to where the largest is
     // 2^7: after the first pages that is rare, and so are the maxima over the rows (the 8 lanes
     // sharing t) and the rescale.
@@ -326,14 +393,17 @@ struct PageWarp<bf16, D, G> {
       pb[i][1] = *reinterpret_cast<const __half2*>(&vt);
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 16 + 2 * t;
+      // row g of A: the scales of block g
+      const uint32_t za = g < NB ? *reinterpret_cast<const uint32_t*>(pg + P::v_scale(g, r)) : 0u;
+      const uint32_t zb = g < NB ? *reinterpret_cast<const uint32_t*>(pg + P::v_scale(g, r + 8)) : 0u;
+      mma_f16_16816(off, za, 0u, zb, 0u, as_u32(pb[i][0]), as_u32(pb[i][1]), off[0], off[1], off[2],
+                    off[3]);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int r = i * 16 + 2 * t;
-        const __half2 wu = __hmul2(pb[i][0], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r)));
-        const __half2 wv = __hmul2(pb[i][1], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r + 8)));
-        const uint32_t w0 = *reinterpret_cast<const uint32_t*>(&wu);
-        const uint32_t w1 = *reinterpret_cast<const uint32_t*>(&wv);
+        const uint32_t w0 = as_u32(__hmul2(pb[i][0], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r))));
+        const uint32_t w1 = as_u32(__hmul2(pb[i][1], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r + 8))));
         const uint32_t va = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r, g));
         const uint32_t vb = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r + 8, g));
         float(&X)[4] = O[b][0];
@@ -341,14 +411,8 @@ struct PageWarp<bf16, D, G> {
         const uint32_t ua = va >> 8, ub = vb >> 8;
         float(&Y)[4] = O[b][1];
         mma_f16_16816(Y, ua & LO, ua & HI, ub & LO, ub & HI, w0, w1, Y[0], Y[1], Y[2], Y[3]);
-        uint32_t z0 = w0, z1 = w1;
-        if (poison) {       // 0 x NaN would reach the other blocks' rows; X and Y have it already
-          z0 &= __heq2_mask(wu, wu);
-          z1 &= __heq2_mask(wv, wv);
-        }
-        const uint32_t one = g == b ? 0x00080008u : 0u;
-        mma_f16_16816(off, one, 0u, one, 0u, z0, z1, off[0], off[1], off[2], off[3]);
       }
+    }
   }
 
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
@@ -361,8 +425,9 @@ struct PageWarp<bf16, D, G> {
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const float z0 = __shfl_sync(0xffffffffu, off[0], b * 4 + t) * kUp;
-      const float z1 = __shfl_sync(0xffffffffu, off[1], b * 4 + t) * kUp;
+      float z0 = __shfl_sync(0xffffffffu, off[0], b * 4 + t) * 8.f;
+      float z1 = __shfl_sync(0xffffffffu, off[1], b * 4 + t) * 8.f;
+      if (poison >> b & 1u) z0 = z1 = NAN;
       const float(&X)[4] = O[b][0], (&Y)[4] = O[b][1];
       if (2 * t < G)
         *reinterpret_cast<float4*>(sa + 2 * t * D + b * 32 + g * 4) =
@@ -386,371 +451,622 @@ struct PageWarp<bf16, D, G> {
   }
 };
 
+// The pages one warp works through, in its own ring of ST stages of shared memory. Page k of the
+// warp is entry k mod 32 (one per lane) of list k / 32: page number << 6 | rows that count, 0 for
+// nothing to read. Two lists are held, the one being worked on and the next; `fill` makes them.
+template <int D, int ST>
+struct PageRing {
+  using P = PageLayout<D>;
+  unsigned char* pages;
+  unsigned char* ring;
+  uint64_t* full;
+  uint32_t list, next;
+  int k, stage;
+  uint32_t phase;                // bit s: parity of stage s
+
+  __device__ __forceinline__ void issue(int s, uint32_t e, int lane) {
+    if (e != 0u && lane == 0) {
+      mbar_arrive_expect_tx(&full[s], P::kBytes);
+      bulk_load(ring + s * P::kBytes, pages + (size_t)(e >> 6) * P::kBytes, P::kBytes, &full[s]);
+    }
+  }
+  // `first` is list 0. The copies of the first ST pages go out.
+  __device__ __forceinline__ void start(unsigned char* pages_, unsigned char* ring_, uint64_t* full_,
+                                        uint32_t first, int lane) {
+    pages = pages_;
+    ring = ring_;
+    full = full_;
+    next = first;
+    list = 0u;
+    k = stage = 0;
+    phase = 0u;
+    if (lane == 0) {
+      for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
+      fence_mbar_init();
+    }
+    __syncwarp();
+#pragma unroll
+    for (int s = 0; s < ST; ++s) issue(s, __shfl_sync(0xffffffffu, next, s), lane);
+  }
+  // Hands the pages up to (not including) page `kend` to take(page in shared memory, rows).
+  // False when a copy did not arrive: the warp's other copies have had their bound by then, and
+  // none is issued any more.
+  template <typename Fill, typename Take>
+  __device__ __forceinline__ bool run(int kend, int lane, Fill&& fill, Take&& take) {
+    for (; k < kend; ++k) {
+      if ((k & 31) == 0) {
+        list = next;
+        next = fill();
+      }
+      const uint32_t cur = __shfl_sync(0xffffffffu, list, k & 31);
+      if (cur != 0u) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase >> stage & 1u))) {
+          for (int i = 0; i < ST; ++i) {
+            const uint32_t e = __shfl_sync(0xffffffffu, (k & 31) + i < 32 ? list : next, (k + i) & 31);
+            const int s = (stage + i) % ST;
+            if (e != 0u) mbar_wait(&full[s], phase >> s & 1u);
+          }
+          return false;
+        }
+        phase ^= 1u << stage;
+        take(ring + stage * P::kBytes, (int)(cur & 63u));
+        __syncwarp();
+      }
+      issue(stage, __shfl_sync(0xffffffffu, (k & 31) + ST < 32 ? list : next, (k + ST) & 31), lane);
+      stage = stage + 1 == ST ? 0 : stage + 1;
+    }
+    return true;
+  }
+};
+
+// What a decode call works on.
+template <typename T>
+struct PageArgs {
+  const T* q;
+  unsigned char* pages;
+  const int32_t* table;
+  int n_pages, max_pages;
+  int32_t* len;
+  const T* k_new;              // nullptr: nothing to append
+  const T* v_new;
+  T* out;
+  int units;
+  int32_t* counters;
+  int32_t* done;
+  float* part;
+  int32_t* flags;
+
+  __device__ __forceinline__ int legal(int L) const {
+    return L < 0 || L > (long long)max_pages * kPageRows ? 0 : L;
+  }
+  // The page a new row of unit u goes to, -1 when it has none (or its length is out of range).
+  __device__ __forceinline__ int new_page(int u, int L) const {
+    if (k_new == nullptr || L < 0 || L / kPageRows >= max_pages) return -1;
+    const int id = table[(size_t)u * max_pages + L / kPageRows];
+    return id >= 0 && id < n_pages ? id : -1;
+  }
+};
+
+// Logit (log2) of the new row for query head g of unit u; count 1, so no bias. A whole warp.
+template <typename T, int D, int G>
+__device__ __forceinline__ float new_logit(const PageArgs<T>& a, int u, int g, int lane) {
+  float sp = 0.f;
+#pragma unroll
+  for (int c = 0; c < D / 32; ++c)
+    sp = fmaf(to_f32(a.q[((size_t)u * G + g) * D + c * 32 + lane]),
+              to_f32(a.k_new[(size_t)u * D + c * 32 + lane]), sp);
+  return warp_sum(sp) * (kLog2e / sqrtf((float)D));
+}
+
+// Four columns of an output from the sum A over a unit's rows (weights against M, their sum Ls)
+// and the new row (logit sn, -inf for none).
+template <typename T>
+__device__ __forceinline__ void finish_columns(float4 A, float M, float Ls, float sn, const T* vn, T* o) {
+  if (sn > -INFINITY || sn != sn) {
+    const float R = fmaxf(M, sn);
+    const float fo = Ls != 0.f ? ex2_ftz(M - R) : 0.f, fn = ex2_ftz(sn - R);
+    Ls = fmaf(Ls, fo, fn);
+    A.x = fmaf(A.x, fo, to_f32(vn[0]) * fn);
+    A.y = fmaf(A.y, fo, to_f32(vn[1]) * fn);
+    A.z = fmaf(A.z, fo, to_f32(vn[2]) * fn);
+    A.w = fmaf(A.w, fo, to_f32(vn[3]) * fn);
+  }
+  const float inv = Ls == 0.f ? 0.f : 1.f / Ls;      // 0: nothing attended, zeros
+  store_out<T>(o, A.x * inv);
+  store_out<T>(o + 1, A.y * inv);
+  store_out<T>(o + 2, A.z * inv);
+  store_out<T>(o + 3, A.w * inv);
+}
+
+// Writes the new row of unit u quantised to row L of page `id`: warp 0 the key, warp 1 the value.
+template <typename T, int D>
+__device__ __forceinline__ void write_new_row(const PageArgs<T>& a, int u, int L, int id, int warp, int lane) {
+  using P = PageLayout<D>;
+  if (warp >= 2) return;
+  const T* src = (warp == 0 ? a.k_new : a.v_new) + (size_t)u * D;
+  float x[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) x[c] = lane < D / 8 ? to_f32(src[lane * 8 + c]) : 0.f;
+  uint32_t sb;
+  const uint32_t w = quantise_lane<T>(x, sb);
+  if (lane >= D / 8) return;
+  unsigned char* pg = a.pages + (size_t)id * P::kBytes;
+  const int r = L % kPageRows, b = lane / 4, sub = lane % 4;
+  if (warp == 0) {
+    *reinterpret_cast<uint32_t*>(pg + P::k_code(b, r) + sub * 4) = w;
+    if (sub == 0) *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, r)) = (uint16_t)sb;
+    if (lane == 0) *reinterpret_cast<float*>(pg + P::logn(r)) = 0.f;
+  } else {
+    *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, r, sub * 2)) = (uint16_t)w;
+    *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, r, sub * 2 + 1)) = (uint16_t)(w >> 16);
+    if (sub == 0) *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, r)) = (uint16_t)sb;
+  }
+}
+
+// Sum of the warps' partial outputs, four columns from column c of query head g on.
+template <int D, int G, int NW>
+__device__ __forceinline__ float4 merge_warps(const float* s_acc, const float (*s_m)[G], const float (*s_l)[G],
+                                              int g, int c, float& M, float& Ls) {
+  M = -INFINITY;
+  Ls = 0.f;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][g]);
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    const float f = part_weight(s_m[w][g], s_l[w][g], M);
+    const float4 v = *reinterpret_cast<const float4*>(s_acc + (w * G + g) * D + c);
+    A.x = fmaf(v.x, f, A.x); A.y = fmaf(v.y, f, A.y);
+    A.z = fmaf(v.z, f, A.z); A.w = fmaf(v.w, f, A.w);
+    Ls = fmaf(s_l[w][g], f, Ls);
+  }
+  return A;
+}
+
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPdThreads, 2)
-page_decode_kernel(const T* __restrict__ q, unsigned char* pages, const int32_t* __restrict__ table,
-                   int n_pages, int max_pages, int32_t* len, const T* __restrict__ k_new,
-                   const T* __restrict__ v_new, T* __restrict__ out, int units, int32_t* counters,
-                   int32_t* done, float* part, int32_t* flags) {
+page_decode_kernel(const PageArgs<T> a) {
   using P = PageLayout<D>;
   using S = PageDecodeShape<D, G>;
   constexpr int NW = kPdWarps, ST = kPdStages, RS = D + kPartPad;
   extern __shared__ __align__(128) unsigned char dsm[];
-  unsigned char* ring = dsm + (threadIdx.x / 32) * ST * P::kBytes;          // this warp's stages
   float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
-  uint64_t* full = reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc) + (threadIdx.x / 32) * ST;
-  __shared__ __align__(16) float qs[G][D];
-  __shared__ float s_m[NW][G], s_l[NW][G], s_new[G], s_stat[G][2];
-  __shared__ float s_fac[G * NW];
-  __shared__ long long s_sum[NW];
-  __shared__ int s_unit, s_last;
-  __shared__ long long s_at;
+  __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
+  __shared__ float s_m[NW][G], s_l[NW][G], s_stat[G][2];
+  // the new row's logits and page for the unit that began in an earlier CTA (0), the one that
+  // goes on in a later one (1), and units that are whole here (2 and 3 in turn)
+  __shared__ float s_new[4][G];
+  __shared__ int s_page[4];
+  __shared__ int4 s_split[2];     // units 0 and 1: unit, first CTA, CTAs, length
+  __shared__ int s_last[2];
 
   griddep_wait();                 // launched with programmatic stream serialisation
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool want_append = k_new != nullptr;
-  const long long cap = (long long)max_pages * kPageRows;
-  auto length = [&](int u) {
-    const int L = len[u];
-    return L < 0 || L > cap ? 0 : L;
-  };
-  if (lane == 0) {
-    for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
-    fence_mbar_init();
-  }
+  if (tid < 2) s_split[tid].x = -1;
 
-  // the numbering: total pages, and the unit and page this CTA starts with
-  const int per = (units + kPdThreads - 1) / kPdThreads;
-  const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
-  long long mine = 0;
-  for (int u = u0; u < u1; ++u) {
-    const int L = len[u];
-    if ((L < 0 || L > cap) && blockIdx.x == 0) set_flag(flags, KVS_FLAG_BAD_LENGTH);
-    mine += unit_span(length(u));
+  // The numbering: total pages, and the unit and page this CTA starts with. Every warp works it
+  // out for itself, so no barrier comes before the first copies. The host keeps the total below
+  // 2^31.
+  uint32_t sum = 0;
+#pragma unroll 4
+  for (int u = lane; u < a.units; u += 32) {
+    const int L = a.len[u];
+    if (L != a.legal(L) && blockIdx.x == 0 && warp == 0) set_flag(a.flags, KVS_FLAG_BAD_LENGTH);
+    sum += unit_span(a.legal(L));
   }
-  long long inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) s_sum[warp] = inc;
-  __syncthreads();
-  long long total = 0, before = 0;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) {
-    if (w < warp) before += s_sum[w];
-    total += s_sum[w];
-  }
+  const int total = (int)__reduce_add_sync(0xffffffffu, sum);
   // at least one page per warp of a CTA: short caches gain nothing from more partial rows
-  long long chunk = (total + gridDim.x - 1) / gridDim.x;
-  if (chunk < NW) chunk = NW;
-  const long long f0 = blockIdx.x * chunk, f1 = min(total, f0 + chunk);
-  if (f0 < f1) {
-    long long at = before + inc - mine;
-    if (at <= f0 && f0 < at + mine) {
-      int u = u0;
-      for (; at + unit_span(length(u)) <= f0; ++u) at += unit_span(length(u));
-      s_unit = u;
-      s_at = at;
-    }
-  }
-  __syncthreads();
+  const int chunk = max(NW, (total + (int)gridDim.x - 1) / (int)gridDim.x);
+  const int f0 = (int)min((long long)total, (long long)blockIdx.x * chunk);
+  const int f1 = (int)min((long long)total, (long long)f0 + chunk);
 
   if (f0 < f1) {
-    // This warp's pages are f0 + warp, f0 + warp + NW, ... The issuing side runs ST pages ahead
-    // of the consuming side, each with its own place in the numbering.
     struct Place {
       int u, L;
-      long long at, end;           // the unit's pages are [at, end)
+      int at, end;                 // the unit's pages are [at, end)
     };
-    auto move_to = [&](Place& p, long long f) {
+    auto append = [&](int u, int L, int id) {
+      if (id >= 0)
+        write_new_row<T, D>(a, u, L, id, warp, lane);
+      else if (tid == 0 && a.len[u] == L)
+        set_flag(a.flags, KVS_FLAG_OUT_CAPACITY);
+    };
+    auto move_to = [&](Place& p, int f) {
       while (f >= p.end) {
         ++p.u;
-        p.L = length(p.u);
+        p.L = a.legal(a.len[p.u]);
         p.at = p.end;
         p.end = p.at + unit_span(p.L);
       }
     };
-    Place ip{s_unit, length(s_unit), s_at, 0};
-    ip.end = ip.at + unit_span(ip.L);
-    long long fi = f0 + warp;      // next page to issue
-    uint32_t loaded = 0;           // bit s: stage s holds (or is getting) a page
-    auto issue = [&](int s) {
-      loaded &= ~(1u << s);
-      if (fi < f1) {
-        move_to(ip, fi);
-        const long long j = fi - ip.at;
-        if (j * kPageRows < ip.L) {
-          const int id = table[(size_t)ip.u * max_pages + j];
-          if (id >= 0 && id < n_pages) {
-            loaded |= 1u << s;
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&full[s], P::kBytes);
-              bulk_load(ring + s * P::kBytes, pages + (size_t)id * P::kBytes, P::kBytes, &full[s]);
-            }
-          } else if (lane == 0) {
-            set_flag(flags, KVS_FLAG_BAD_PAGE);
-          }
-        }
+    Place cp;
+    {
+      int base = 0, acc = 0, w, n;                 // the 32 units that page f0 falls among
+      for (;; base += 32, acc += n) {
+        w = base + lane < a.units ? unit_span(a.legal(a.len[base + lane])) : 0;
+        n = (int)__reduce_add_sync(0xffffffffu, (uint32_t)w);
+        if (f0 < acc + n) break;
       }
-      fi += NW;
-    };
-    for (int s = 0; s < ST; ++s) issue(s);
+      int inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int who = __ffs(__ballot_sync(0xffffffffu, f0 < acc + inc)) - 1;
+      cp.u = base + who;
+      cp.L = a.legal(a.len[cp.u]);
+      cp.end = acc + __shfl_sync(0xffffffffu, inc, who);
+      cp.at = cp.end - unit_span(cp.L);
+    }
 
-    const float qscale = kLog2e / sqrtf((float)D);
-    Place cp{s_unit, length(s_unit), s_at, 0};
-    cp.end = cp.at + unit_span(cp.L);
-    long long fc = f0 + warp;      // next page to consume
-    int stage = 0;
-    uint32_t phase = 0;            // bit s: parity of stage s
-    for (long long seg = f0; seg < f1;) {
+    // This warp's pages are f0 + warp, f0 + warp + NW, ...
+    Place lp = cp;                 // this lane's place in the list that comes next
+    int lf = f0 + warp + NW * lane;
+    auto fill = [&]() -> uint32_t {
+      uint32_t e = 0;
+      if (lf < f1) {
+        move_to(lp, lf);
+        const int n = min(kPageRows, lp.L - (lf - lp.at) * kPageRows);
+        if (n > 0) {
+          const int id = a.table[(size_t)lp.u * a.max_pages + (lf - lp.at)];
+          if (id >= 0 && id < a.n_pages)
+            e = (uint32_t)id << 6 | (uint32_t)n;
+          else
+            set_flag(a.flags, KVS_FLAG_BAD_PAGE);
+        }
+        lf += 32 * NW;
+      }
+      return e;
+    };
+    // the queries ahead of the pages: behind 150 KB of copies per SM they would come
+    // microseconds later
+    PageWarp<T, D, G> pw;
+    pw.load(a.q + (size_t)cp.u * G * D, lane);
+    PageRing<D, ST> pr;
+    pr.start(a.pages, dsm + warp * ST * P::kBytes,
+             reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc) + warp * ST, fill(), lane);
+
+    int whole = 2;
+    for (int seg = f0; seg < f1;) {
       move_to(cp, seg);
       const int u = cp.u, L = cp.L;
-      const long long seg_end = min(f1, cp.end);
-      for (int i = tid; i < G * D; i += kPdThreads)
-        qs[i / D][i % D] = to_f32(q[(size_t)u * G * D + i]) * qscale;
-      __syncthreads();
-
-      PageWarp<T, D, G> pw;
-      pw.begin(q + (size_t)u * G * D, qs, lane);
-      for (; fc < seg_end; fc += NW) {
-        const int nval = (int)min((long long)kPageRows, L - (fc - cp.at) * kPageRows);
-        if (loaded >> stage & 1u) {
-          if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase >> stage & 1u))) {
-            // give up: give every copy in flight one more bound, then take no further page
-            set_flag(flags, KVS_FLAG_TIMEOUT);
-            for (int s = 0; s < ST; ++s)
-              if (loaded >> s & 1u) mbar_wait(&full[s], phase >> s & 1u);
-            loaded = 0;
-            fi = f1;
-            continue;
-          }
-          phase ^= 1u << stage;
-          pw.take(ring + stage * P::kBytes, nval, lane);
-          __syncwarp();
-        }
-        issue(stage);
-        stage = stage + 1 == ST ? 0 : stage + 1;
+      const int seg_end = min(f1, cp.end);
+      const int first = cp.at / chunk, nsplit = (cp.end - 1) / chunk - first + 1;
+      const int slot = nsplit == 1 ? whole : (int)blockIdx.x == first ? 1 : 0;
+      if constexpr (sizeof(T) == 4) {
+        for (int i = tid; i < G * D; i += kPdThreads)
+          (&qs[0][0])[i] = to_f32(a.q[(size_t)u * G * D + i]) * (kLog2e / sqrtf((float)D));
+        __syncthreads();
       }
+      pw.begin(reinterpret_cast<const float(*)[D]>(qs), lane);
+      if (a.k_new != nullptr) {    // while the pages are on their way
+        const int id = a.new_page(u, a.len[u]);
+        if (id >= 0 && warp < G) {
+          const float sn = new_logit<T, D, G>(a, u, warp, lane);
+          if (lane == 0) s_new[slot][warp] = sn;
+        }
+        if (tid == 0) s_page[slot] = id;
+      }
+      static_assert(G <= NW, "a warp per query head");
+      if (!pr.run((seg_end - f0 - warp + NW - 1) / NW, lane, fill,
+                  [&](unsigned char* pg, int n) { pw.take(pg, n, lane); })) {
+        set_flag(a.flags, KVS_FLAG_TIMEOUT);
+        pr.next = pr.list = 0u;
+        lf = f1;
+      }
+      if (seg_end < f1) pw.load(a.q + (size_t)(u + 1) * G * D, lane);
+      if (seg != f0) __syncthreads();              // the last unit's partials have been read
       pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
-
-      // ---- the end of the unit in this CTA ----
-      const long long lp = L / kPageRows;            // the page a new row goes to
-      int new_id = -1;
-      if (want_append && len[u] == L && lp < max_pages) new_id = table[(size_t)u * max_pages + lp];
-      const bool fits = new_id >= 0 && new_id < n_pages;
-      if (fits)
-        for (int g = warp; g < G; g += NW) {
-          float sp = 0.f;
-          for (int c = lane; c < D; c += 32) sp = fmaf(qs[g][c], to_f32(k_new[(size_t)u * D + c]), sp);
-          sp = warp_sum(sp);
-          if (lane == 0) s_new[g] = sp;
-        }
       __syncthreads();
-      const long long first = cp.at / chunk, last = (cp.end - 1) / chunk;
-      const int nsplit = (int)(last - first) + 1;
-      bool finish = true;
-      if (nsplit > 1) {
-        // slot 1 of the CTA the unit begins in, slot 0 of the others
-        float* row0 = part + ((size_t)blockIdx.x * 2 + (blockIdx.x == first ? 1 : 0)) * G * RS;
-        for (int i = tid; i < G * D; i += kPdThreads) {
-          const int g = i / D, c = i % D;
-          float M = -INFINITY, A = 0.f, Ls = 0.f;
-          for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][g]);
-          for (int w = 0; w < NW; ++w) {
-            const float f = part_weight(s_m[w][g], s_l[w][g], M);
-            A = fmaf(s_acc[(w * G + g) * D + c], f, A);
-            Ls = fmaf(s_l[w][g], f, Ls);
-          }
-          row0[g * RS + c] = A;
-          if (c == 0) {
-            row0[g * RS + D] = M;
-            row0[g * RS + D + 1] = Ls;
-          }
+      if (tid < G * D / 4) {
+        const int g = tid * 4 / D, c = tid * 4 % D;
+        float M, Ls;
+        const float4 A = merge_warps<D, G, NW>(s_acc, s_m, s_l, g, c, M, Ls);
+        if (nsplit == 1) {
+          const bool fits = a.k_new != nullptr && s_page[slot] >= 0;
+          finish_columns<T>(A, M, Ls, fits ? s_new[slot][g] : -INFINITY, a.v_new + (size_t)u * D + c,
+                            a.out + (size_t)u * G * D + tid * 4);
+        } else {
+          // a row of the workspace; who finishes the unit is settled after this CTA's last page
+          float* row = a.part + ((size_t)blockIdx.x * 2 + slot) * G * RS + g * RS;
+          *reinterpret_cast<float4*>(row + c) = A;
+          if (c == 0) *reinterpret_cast<float2*>(row + D) = make_float2(M, Ls);
         }
-        __syncthreads();
-        if (tid == 0) s_last = atom_add_acq_rel_gpu(&counters[u], 1) == nsplit - 1;
-        __syncthreads();
-        finish = s_last != 0;
       }
-      if (finish) {
-        // Sum the partials (the splits' rows in the workspace, or the warps' in shared memory):
-        // four columns a thread, the partials dealt out over NGRP threads for each four. The
-        // workspace rows are loaded in batches ahead of the factors, one round trip a batch.
-        constexpr int NU = S::kUnits, NGRP = S::kGroups;
-        constexpr int kBatch = 8;
-        const int grp = tid / NU, unit = tid % NU, g = unit * 4 / D, c = unit * 4 % D;
-        const int np = nsplit > 1 ? nsplit : NW;
-        auto row_of = [&](int s) {
-          return part + ((size_t)(first + s) * 2 + (s == 0 ? 1 : 0)) * G * RS;
-        };
-        float4 v[kBatch];
-        if (nsplit > 1) {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (grp + i * NGRP < np)
-              v[i] = __ldcg(reinterpret_cast<const float4*>(row_of(grp + i * NGRP) + g * RS + c));
-        }
-        float* fac = nsplit > 1 ? s_acc : s_fac;     // [G][np]
-        for (int gg = warp; gg < G; gg += NW) {
-          const float sn = fits ? s_new[gg] : -INFINITY;
-          constexpr int kMaxPer = (kPageDecodeCtas + 31) / 32;
-          float ms[kMaxPer], ls[kMaxPer], M = sn;
-#pragma unroll
-          for (int i = 0; i < kMaxPer; ++i) {
-            const int s = lane + i * 32;
-            ms[i] = -INFINITY;
-            ls[i] = 0.f;
-            if (s < np) {
-              if (nsplit > 1) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2*>(row_of(s) + gg * RS + D));
-                ms[i] = ml.x;
-                ls[i] = ml.y;
-              } else {
-                ms[i] = s_m[s][gg];
-                ls[i] = s_l[s][gg];
-              }
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < kMaxPer; ++i) M = fmaxf(M, ms[i]);
-          M = warp_max(M);
-          float Ls = 0.f;
-#pragma unroll
-          for (int i = 0; i < kMaxPer; ++i) {
-            const int s = lane + i * 32;
-            const float f = part_weight(ms[i], ls[i], M);
-            Ls = fmaf(ls[i], f, Ls);
-            if (s < np) fac[gg * np + s] = f;
-          }
-          Ls = warp_sum(Ls);
-          if (sn > -INFINITY) Ls += exp2f(sn - M);
-          if (lane == 0) {
-            s_stat[gg][0] = M;
-            s_stat[gg][1] = Ls;
-          }
-        }
-        __syncthreads();
-        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s0 = grp; s0 < np; s0 += kBatch * NGRP) {
-          if (nsplit > 1) {
-            if (s0 != grp) {
-#pragma unroll
-              for (int i = 0; i < kBatch; ++i)
-                if (s0 + i * NGRP < np)
-                  v[i] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + i * NGRP) + g * RS + c));
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i)
-              if (s0 + i * NGRP < np)
-                v[i] = *reinterpret_cast<const float4*>(s_acc + ((s0 + i * NGRP) * G + g) * D + c);
-          }
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (s0 + i * NGRP < np) {
-              const float f = fac[g * np + s0 + i * NGRP];
-              A.x = fmaf(v[i].x, f, A.x);
-              A.y = fmaf(v[i].y, f, A.y);
-              A.z = fmaf(v[i].z, f, A.z);
-              A.w = fmaf(v[i].w, f, A.w);
-            }
-        }
-        if constexpr (NGRP > 1) {
-          __syncthreads();                           // the warps' partials have been read
-          if (grp > 0) *reinterpret_cast<float4*>(s_acc + S::kFac / 4 + ((grp - 1) * NU + unit) * 4) = A;
-          __syncthreads();
-          if (grp == 0)
-#pragma unroll
-            for (int i = 0; i < NGRP - 1; ++i) {
-              const float4 w = *reinterpret_cast<const float4*>(s_acc + S::kFac / 4 + (i * NU + unit) * 4);
-              A.x += w.x; A.y += w.y; A.z += w.z; A.w += w.w;
-            }
-        }
-        if (grp == 0) {
-          const float M = s_stat[g][0], Ls = s_stat[g][1];
-          if (fits) {
-            const float f = exp2f(s_new[g] - M);
-            const T* vn = v_new + (size_t)u * D + c;
-            A.x = fmaf(to_f32(vn[0]), f, A.x); A.y = fmaf(to_f32(vn[1]), f, A.y);
-            A.z = fmaf(to_f32(vn[2]), f, A.z); A.w = fmaf(to_f32(vn[3]), f, A.w);
-          }
-          T* o = out + (size_t)u * G * D + unit * 4;
-          const bool none = Ls == 0.f;               // nothing attended: zeros
-          store_out<T>(o, none ? 0.f : A.x / Ls);
-          store_out<T>(o + 1, none ? 0.f : A.y / Ls);
-          store_out<T>(o + 2, none ? 0.f : A.z / Ls);
-          store_out<T>(o + 3, none ? 0.f : A.w / Ls);
-        }
-        if (want_append && len[u] == L) {
-          if (fits) {
-            if (warp < 2) {
-              // warp 0 the key, warp 1 the value: 8 channels a lane
-              const T* src = (warp == 0 ? k_new : v_new) + (size_t)u * D;
-              float x[8];
-#pragma unroll
-              for (int c = 0; c < 8; ++c) x[c] = lane < D / 8 ? to_f32(src[lane * 8 + c]) : 0.f;
-              uint32_t sb;
-              const uint32_t w = quantise_lane<T>(x, sb);
-              unsigned char* pg = pages + (size_t)new_id * P::kBytes;
-              const int r = L % kPageRows, b = lane / 4, sub = lane % 4;
-              if (lane < D / 8) {
-                if (warp == 0) {
-                  *reinterpret_cast<uint32_t*>(pg + P::k_code(b, r) + sub * 4) = w;
-                  if (sub == 0) *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, r)) = (uint16_t)sb;
-                  if (lane == 0) *reinterpret_cast<float*>(pg + P::logn(r)) = 0.f;
-                } else {
-                  *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, r, sub * 2)) = (uint16_t)w;
-                  *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, r, sub * 2 + 1)) = (uint16_t)(w >> 16);
-                  if (sub == 0) *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, r)) = (uint16_t)sb;
-                }
-              }
-            }
-          } else if (tid == 0) {
-            set_flag(flags, KVS_FLAG_OUT_CAPACITY);
-          }
-        }
-        if (tid == 0 && nsplit > 1) counters[u] = 0;
+      if (nsplit == 1) {
+        if (a.k_new != nullptr) append(u, L, s_page[slot]);
+        whole ^= 1;
+      } else if (tid == 0) {
+        s_split[slot] = make_int4(u, first, nsplit, L);
       }
       seg = seg_end;
-      __syncthreads();            // the shared arrays are free for the next unit
+    }
+
+    // Who finishes the units split over several CTAs: the last of them to arrive here. (That
+    // costs a round trip to L2, so it waits until this CTA's pages are through.)
+    __syncthreads();
+    if (tid < 2) {
+      const int4 sp = s_split[tid];
+      s_last[tid] = sp.x >= 0 && atom_add_acq_rel_gpu(&a.counters[sp.x], 1) == sp.z - 1;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      if (!s_last[i]) continue;
+      // Sum the splits' rows: four columns a thread, the splits dealt out over NGRP threads for
+      // each four, loads in batches.
+      constexpr int NU = S::kUnits, NGRP = S::kGroups, kBatch = 4;
+      const int4 sp = s_split[i];
+      const int u = sp.x, np = sp.z;
+      const int grp = tid / NU, unit = tid % NU, g = unit * 4 / D, c = unit * 4 % D;
+      // slot 1 of the CTA the unit begins in, slot 0 of the others
+      const float* rows = a.part + (size_t)sp.y * 2 * G * RS;
+      auto row_of = [&](int s) { return rows + (2 * s + (s == 0 ? 1 : 0)) * G * RS; };
+      float* fac = s_acc;                          // [G][np]
+      if (warp < G) {
+        float M = -INFINITY;
+        for (int s = lane; s < np; s += 32) M = fmaxf(M, __ldcg(row_of(s) + warp * RS + D));
+        M = warp_max(M);
+        float Ls = 0.f;
+        for (int s = lane; s < np; s += 32) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(row_of(s) + warp * RS + D));
+          const float f = part_weight(ml.x, ml.y, M);
+          Ls = fmaf(ml.y, f, Ls);
+          fac[warp * np + s] = f;
+        }
+        Ls = warp_sum(Ls);
+        if (lane == 0) {
+          s_stat[warp][0] = M;
+          s_stat[warp][1] = Ls;
+        }
+      }
+      __syncthreads();
+      float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int s0 = grp; s0 < np; s0 += kBatch * NGRP) {
+        float4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s0 + j * NGRP < np)
+            v[j] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + j * NGRP) + g * RS + c));
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s0 + j * NGRP < np) {
+            const float f = fac[g * np + s0 + j * NGRP];
+            A.x = fmaf(v[j].x, f, A.x); A.y = fmaf(v[j].y, f, A.y);
+            A.z = fmaf(v[j].z, f, A.z); A.w = fmaf(v[j].w, f, A.w);
+          }
+      }
+      if constexpr (NGRP > 1) {
+        float* sums = s_acc + S::kFac / 4;
+        if (grp > 0) *reinterpret_cast<float4*>(sums + ((grp - 1) * NU + unit) * 4) = A;
+        __syncthreads();
+        if (grp == 0)
+#pragma unroll
+          for (int j = 0; j < NGRP - 1; ++j) {
+            const float4 w = *reinterpret_cast<const float4*>(sums + (j * NU + unit) * 4);
+            A.x += w.x; A.y += w.y; A.z += w.z; A.w += w.w;
+          }
+      }
+      if (grp == 0) {
+        const bool fits = a.k_new != nullptr && s_page[i] >= 0;
+        finish_columns<T>(A, s_stat[g][0], s_stat[g][1], fits ? s_new[i][g] : -INFINITY,
+                          a.v_new + (size_t)u * D + c, a.out + (size_t)u * G * D + unit * 4);
+      }
+      if (a.k_new != nullptr) append(u, sp.w, s_page[i]);
+      if (tid == 0) a.counters[u] = 0;
+      __syncthreads();            // the shared arrays are free for the other unit
     }
   }
-  if (want_append) {
+  if (a.k_new != nullptr) {
     // every CTA reads every length: they move on once the last CTA is through
     __syncthreads();
-    if (tid == 0) s_last = atom_add_acq_rel_gpu(done, 1) == (int)gridDim.x - 1;
+    if (tid == 0) s_last[0] = atom_add_acq_rel_gpu(a.done, 1) == (int)gridDim.x - 1;
     __syncthreads();
-    if (s_last) {
-      for (int u = tid; u < units; u += kPdThreads) {
-        const int L = len[u];
-        if (L < 0 || L >= cap) continue;
-        const int id = table[(size_t)u * max_pages + L / kPageRows];
-        if (id >= 0 && id < n_pages) len[u] = L + 1;
+    if (s_last[0]) {
+      for (int u = tid; u < a.units; u += kPdThreads) {
+        const int L = a.len[u];
+        if (a.new_page(u, L) >= 0) a.len[u] = L + 1;
       }
-      if (tid == 0) *done = 0;
+      if (tid == 0) *a.done = 0;
     }
   }
+}
+
+// The same with one thread-block cluster per unit, for few units: the CTAs of the cluster take
+// the unit's pages in turn, and combine through distributed shared memory. The page numbers do
+// not depend on the other units' lengths, so they are loaded together with the length, and the
+// combine needs neither the workspace nor a round trip to it.
+template <typename T, int D, int G>
+__global__ void __launch_bounds__(kPcWarps * 32, 1)
+page_decode_cluster_kernel(const PageArgs<T> a) {
+  using P = PageLayout<D>;
+  using S = PageClusterShape<D, G>;
+  constexpr int NW = kPcWarps, ST = kPcStages;
+  extern __shared__ __align__(128) unsigned char dsm[];
+  float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
+  float* s_sum = reinterpret_cast<float*>(dsm + S::kRing + S::kAcc);        // [G][D], read by peers
+  __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
+  __shared__ float s_m[NW][G], s_l[NW][G], s_new[G];
+  __shared__ __align__(8) float s_ml[G][2];                                 // read by peers
+
+  griddep_wait();                 // launched with programmatic stream serialisation
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int u = blockIdx.y, C = gridDim.x, rank = (int)cluster_ctarank();
+  const int len = a.len[u], L = a.legal(len);
+  long long j = rank + (long long)C * (warp + NW * lane);      // this lane's page of list 0
+  int id = j < a.max_pages ? a.table[(size_t)u * a.max_pages + j] : -1;
+  PageWarp<T, D, G> pw;
+  pw.load(a.q + (size_t)u * G * D, lane);
+  if (L != len && rank == 0 && tid == 0) set_flag(a.flags, KVS_FLAG_BAD_LENGTH);
+  auto entry = [&]() -> uint32_t {
+    const int n = (int)min((long long)kPageRows, L - j * kPageRows);
+    if (n <= 0) return 0u;
+    if (id >= 0 && id < a.n_pages) return (uint32_t)id << 6 | (uint32_t)n;
+    set_flag(a.flags, KVS_FLAG_BAD_PAGE);
+    return 0u;
+  };
+  auto fill = [&]() -> uint32_t {
+    j += (long long)C * NW * 32;
+    if (j * kPageRows >= L) return 0u;
+    id = a.table[(size_t)u * a.max_pages + j];
+    return entry();
+  };
+  PageRing<D, ST> pr;
+  pr.start(a.pages, dsm + warp * ST * P::kBytes,
+           reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc + S::kSum) + warp * ST, entry(), lane);
+  if constexpr (sizeof(T) == 4) {
+    for (int i = tid; i < G * D; i += NW * 32)
+      (&qs[0][0])[i] = to_f32(a.q[(size_t)u * G * D + i]) * (kLog2e / sqrtf((float)D));
+    __syncthreads();
+  }
+  pw.begin(reinterpret_cast<const float(*)[D]>(qs), lane);
+  const int new_id = a.k_new != nullptr ? a.new_page(u, len) : -1;
+  if (new_id >= 0 && warp < G) {
+    const float sn = new_logit<T, D, G>(a, u, warp, lane);
+    if (lane == 0) s_new[warp] = sn;
+  }
+  const int np = pages_of(L);
+  if (!pr.run((np - rank + C * (NW - warp) - 1) / (C * NW), lane, fill,
+              [&](unsigned char* pg, int n) { pw.take(pg, n, lane); }))
+    set_flag(a.flags, KVS_FLAG_TIMEOUT);
+  pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
+  __syncthreads();
+  for (int i = tid; i < G * D / 4; i += NW * 32) {
+    const int g = i * 4 / D, c = i * 4 % D;
+    float M, Ls;
+    *reinterpret_cast<float4*>(s_sum + i * 4) = merge_warps<D, G, NW>(s_acc, s_m, s_l, g, c, M, Ls);
+    if (c == 0) {
+      s_ml[g][0] = M;
+      s_ml[g][1] = Ls;
+    }
+  }
+  cluster_arrive();
+  cluster_wait();
+  // this CTA's slice of the output: a half-warp per four columns, lane j of it taking CTA j
+  constexpr int NU = G * D / 4;
+  const int lo = NU * rank / C, hi = NU * (rank + 1) / C;
+  for (int b0 = lo + 2 * warp; b0 < hi; b0 += 2 * NW) {
+    const int b = b0 + (lane >> 4), src = lane & 15;
+    const int g = min(b, NU - 1) * 4 / D, c = b * 4 % D;
+    float m = -INFINITY, l = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (b < hi && src < C) {
+      const float2 ml = ld_cluster_f32x2(cluster_map(smem_u32(&s_ml[g][0]), src));
+      A = ld_cluster_f32x4(cluster_map(smem_u32(s_sum + b * 4), src));
+      m = ml.x;
+      l = ml.y;
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float f = part_weight(m, l, M);
+    l *= f;
+    A.x *= f; A.y *= f; A.z *= f; A.w *= f;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      l += __shfl_xor_sync(0xffffffffu, l, o);
+      A.x += __shfl_xor_sync(0xffffffffu, A.x, o);
+      A.y += __shfl_xor_sync(0xffffffffu, A.y, o);
+      A.z += __shfl_xor_sync(0xffffffffu, A.z, o);
+      A.w += __shfl_xor_sync(0xffffffffu, A.w, o);
+    }
+    if (b < hi && src == 0)
+      finish_columns<T>(A, M, l, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
+                        a.out + (size_t)u * G * D + b * 4);
+  }
+  cluster_arrive();               // this CTA has read its peers; the wait is at the end
+  if (rank == 0 && a.k_new != nullptr) {
+    // every CTA of the cluster read the length before the first barrier
+    if (new_id >= 0) {
+      write_new_row<T, D>(a, u, len, new_id, warp, lane);
+      if (tid == 0) a.len[u] = len + 1;
+    } else if (tid == 0 && len == L) {
+      set_flag(a.flags, KVS_FLAG_OUT_CAPACITY);
+    }
+  }
+  cluster_wait();                 // no CTA leaves while a peer may read its shared memory
+}
+
+// Cluster size for a cluster per unit on the current device, or 0 when the split kernel is to be
+// used: the largest C <= 16 with C * units <= SM count for which the occupancy calculator places
+// all clusters at once. Cached per device and number of units.
+template <typename T, int D, int G>
+static int page_cluster_size(int units) {
+  using S = PageClusterShape<D, G>;
+  auto kfn = page_decode_cluster_kernel<T, D, G>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  static std::mutex mu;
+  static std::map<std::pair<int, int>, int> cache;
+  std::lock_guard<std::mutex> lock(mu);
+  const auto key = std::make_pair(dev, units);
+  const auto it = cache.find(key);
+  if (it != cache.end()) return it->second;
+  int sms = 0;
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int C = sms / units;
+  if (C > kMaxClusterSize) C = kMaxClusterSize;
+  if (!ensure_smem_attr((const void*)kfn, S::kSmem)) C = 0;
+  if (C > 8 && !ensure_nonportable_cluster((const void*)kfn)) C = 8;
+  for (; C >= 2; --C) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C, units);
+    cfg.blockDim = dim3(kPcWarps * 32);
+    cfg.dynamicSmemBytes = S::kSmem;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = C;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void*)kfn, &cfg) == cudaSuccess && n >= units) break;
+  }
+  (void)cudaGetLastError();   // a refused query leaves no error behind
+  if (C < 2) C = 0;
+  cache[key] = C;
+  return C;
 }
 
 template <typename T, int D, int G>
 static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_page_pool& pool,
                             int32_t* len, const void* k_new, const void* v_new, void* out,
                             char* ws, cudaStream_t st) {
-  using S = PageDecodeShape<D, G>;
-  auto kfn = page_decode_kernel<T, D, G>;
-  if (!ensure_smem_attr((const void*)kfn, S::kSmem)) return cudaErrorInvalidValue;
   const int units = d.B * d.H_kv;
   const PageLayoutWs Ly = page_layout_ws(d);
-  const cudaError_t e = launch_pdl(
-      kfn, dim3(kPageDecodeCtas), dim3(kPdThreads), S::kSmem, st, (const T*)q,
-      (unsigned char*)pool.pages, (const int32_t*)pool.table, pool.n_pages, pool.max_pages, len,
-      (const T*)k_new, (const T*)v_new, (T*)out, units, reinterpret_cast<int32_t*>(ws + Ly.counters),
-      reinterpret_cast<int32_t*>(ws + Ly.done), reinterpret_cast<float*>(ws + Ly.part),
-      reinterpret_cast<int32_t*>(ws));
+  const PageArgs<T> a = {(const T*)q, (unsigned char*)pool.pages, pool.table, pool.n_pages,
+                         pool.max_pages, len, (const T*)k_new, (const T*)v_new, (T*)out, units,
+                         reinterpret_cast<int32_t*>(ws + Ly.counters),
+                         reinterpret_cast<int32_t*>(ws + Ly.done),
+                         reinterpret_cast<float*>(ws + Ly.part), reinterpret_cast<int32_t*>(ws)};
   count_launches(1);
+  const int C = page_cluster_size<T, D, G>(units);
+  if (C >= 2 && use_cluster(C, pool.max_pages)) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(C, units);
+    cfg.blockDim = dim3(kPcWarps * 32);
+    cfg.dynamicSmemBytes = PageClusterShape<D, G>::kSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = C;
+    at[1].val.clusterDim.y = 1;
+    at[1].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 2;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, page_decode_cluster_kernel<T, D, G>, a);
+    return e != cudaSuccess ? e : cudaGetLastError();
+  }
+  auto kfn = page_decode_kernel<T, D, G>;
+  using S = PageDecodeShape<D, G>;
+  if (!ensure_smem_attr((const void*)kfn, S::kSmem)) return cudaErrorInvalidValue;
+  const cudaError_t e = launch_pdl(kfn, dim3(kPageDecodeCtas), dim3(kPdThreads), S::kSmem, st, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

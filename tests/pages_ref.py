@@ -84,14 +84,28 @@ def rows_of(pages, table, n, d):
     return np.array(k), np.array(v), np.array(ln)
 
 
+def value_scales(pages, table, n, d):
+    """The scales [n, d / 32] of the values of rows 0 .. n - 1."""
+    out = np.zeros((n, d // 32))
+    for t in range(n):
+        pg = pages[int(table[t // PAGE])]
+        at = _offsets(d, t % PAGE)[3]
+        out[t] = np.array([int(pg[o]) | int(pg[o + 1]) << 8 for o in at], np.uint16).view(np.float16)
+    return out
+
+
+def weights(q, k, logn):
+    x = q @ k.T / np.sqrt(q.shape[1]) + logn
+    p = np.exp(x - x.max(-1, keepdims=True))
+    return p / p.sum(-1, keepdims=True)
+
+
 def attend(q, k, v, logn):
     """(out, size): softmax attention of queries q [G, d], and sum_t p_t |v_t|, which errors of
     the weights scale with. Nothing to attend: zeros."""
     if len(k) == 0 or np.all(logn == -np.inf):
         return np.zeros_like(q), np.zeros_like(q)
-    x = q @ k.T / np.sqrt(q.shape[1]) + logn
-    p = np.exp(x - x.max(-1, keepdims=True))
-    p /= p.sum(-1, keepdims=True)
+    p = weights(q, k, logn)
     return p @ v, p @ np.abs(v)
 
 

@@ -5,10 +5,12 @@ that is derived, with A = sum_t p_t |v_t| and n rows:
   fp32  d + 6 roundings of a logit's products and sums, each half a last place of at most
         X = sum |q k| / sqrt(d) (+ |logn|), make the weights off by 2 (d + 6) 2^-24 X relative;
         n + 16 roundings of the sums and the exponential's 2^-22 add to that.
-  bf16  in addition: the weight is rounded to half twice (alone, and times the row's scale),
-        2 * 2^-11, on the scale of A plus eight times the scale for the codes' offset; weights
-        below the half range are off by at most 2^-25 each, the largest being at least 2^6; and
-        the output is rounded to bf16, 2^-8 |out|.
+  bf16  in addition, with s the scale of a value's block and S = sum_t p_t s_t:
+        the weight is rounded to half, h(p), which both sums of  sum u w - 8 sum s h(p)  see: 2^-11 A;
+        w = half(s h(p)) is seen by the first one only, where the code u is at most 15: 15 2^-11 S;
+        weights (and w) below the half range are off by at most 2^-25 each, the largest p being at
+        least 2^7 over the largest scale above 1: n 2^-32 max(1, s) (|v| + 15 s), and the logit's
+        offset sum is held to 2^-33 of it; and the output is rounded to bf16, 2^-8 |out|.
 """
 
 import gc
@@ -246,17 +248,24 @@ def test_slots_past_the_pool_are_skipped(kvs):
 # Decode attention
 # ---------------------------------------------------------------------------
 
+@pytest.fixture(params=[0, 5000], ids=["short-tables", "wide-tables"])
+def wide(request):
+    """Columns added to the page tables: few units with short tables are decoded by a cluster of
+    CTAs each, long tables (and many units) by the kernel that splits the pages evenly."""
+    return request.param
+
+
 class Cache:
     """A paged cache of given lengths with random pages; unused rows and pages hold garbage."""
 
     def __init__(self, kvs, B, H, G, d, lens, dtype, seed=0, room=1, logn_scale=1.0, v_scale=1.0,
-                 k_scale=1.0):
+                 k_scale=1.0, wide=0):
         self.kvs, self.B, self.H, self.G, self.d, self.dtype = kvs, B, H, G, d, dtype
         rng = self.rng = np.random.default_rng(seed)
         lens = self.lens_np = np.asarray(lens, np.int64)
         units = B * H
         held = -(-(lens + room) // PAGE)
-        maxp = int(held.max()) + 1
+        maxp = int(held.max()) + 1 + wide
         total = int(held.sum()) + 2
         order = rng.permutation(total)
         self.table_np = -np.ones((units, maxp), np.int64)
@@ -303,7 +312,8 @@ class Cache:
                 v = np.concatenate([v, v_new.double().cpu().numpy().reshape(units, 1, d)[u]])
                 ln = np.append(ln, 0.0)
             want, size = ref.attend(q[u], k, v, ln)
-            bound = tolerance(self.dtype, q[u], k, v, ln, want, size)
+            scales = ref.value_scales(self.pages_np, self.table_np[u], int(self.lens_np[u]), d)
+            bound = tolerance(self.dtype, q[u], k, v, ln, want, size, scales)
             err = np.abs(got[u] - want)
             assert np.all(err <= bound), (u, len(k), float((err / bound).max()))
             worst = max(worst, float((err / np.maximum(bound, 1e-300)).max()))
@@ -321,7 +331,7 @@ class Cache:
         assert self.lens.tolist() == self.lens_np.tolist()
 
 
-def tolerance(dtype, q, k, v, logn, want, size):
+def tolerance(dtype, q, k, v, logn, want, size, scales=None):
     n, d = max(1, len(k)), q.shape[1]
     if len(k) == 0:
         return np.zeros_like(want)
@@ -329,9 +339,11 @@ def tolerance(dtype, q, k, v, logn, want, size):
     rel = 2 * (d + 6) * 2.0 ** -24 * x + (n + 16) * 2.0 ** -24 + 2.0 ** -21
     if dtype == torch.float32:
         return rel * size + 2.0 ** -24 * np.abs(want) + 1e-30
-    scale = np.abs(v).max(0, keepdims=True) * 8 / 7 * 1.01         # eight times a row's scale at most
-    top = float(np.abs(v).max())
-    return (rel + 2 * 2.0 ** -11) * (size + scale) + n * 2.0 ** -27 * max(1.0, top) * (1 + top) + 2.0 ** -8 * np.abs(want)
+    s = np.zeros_like(v)                            # the new row, if there is one, is not rounded
+    s[:len(scales)] = np.repeat(scales, 32, 1)
+    p = ref.weights(q, k, logn)
+    low = n * 2.0 ** -32 * max(1.0, float(s.max())) * (np.abs(v) + 15 * s).max(0)
+    return (rel + 2.0 ** -11) * size + 15 * 2.0 ** -11 * (p @ s) + low + 2.0 ** -8 * np.abs(want)
 
 
 EDGE = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 255, 256, 257]
@@ -340,8 +352,8 @@ EDGE = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 255, 256, 257]
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
-def test_decode_at_the_edges_of_pages(kvs, dtype, d, G):
-    c = Cache(kvs, 2, 8, G, d, EDGE, dtype, seed=G + d)
+def test_decode_at_the_edges_of_pages(kvs, dtype, d, G, wide):
+    c = Cache(kvs, 2, 8, G, d, EDGE, dtype, seed=G + d, wide=wide)
     q, kn, vn = c.random(2, 8 * G, d, scale=1.5), c.random(2, 8, d), c.random(2, 8, d)
     c.check(q, c.step(q))
     assert c.lens.tolist() == EDGE and np.array_equal(c.pages.cpu().numpy(), c.pages_np)
@@ -357,9 +369,11 @@ def test_decode_at_the_edges_of_pages(kvs, dtype, d, G):
     (torch.float32, 128, 2, [3001]),
     (torch.bfloat16, 64, 8, [2500, 3, 0, 1777]),
     (torch.bfloat16, 128, 8, [1, 4097, 1, 31]),
-    (torch.float32, 64, 1, [900, 0, 901, 77])])
-def test_decode_of_long_and_ragged_units(kvs, dtype, d, G, lens):
-    c = Cache(kvs, 1, len(lens), G, d, lens, dtype, seed=3, logn_scale=3.0)
+    (torch.float32, 64, 1, [900, 0, 901, 77]),
+    (torch.bfloat16, 128, 4, [1200, 0, 1, 333, 64] * 6),     # some units whole in a CTA, some split
+    (torch.float32, 128, 4, [260, 0, 1, 333, 64] * 6)])
+def test_decode_of_long_and_ragged_units(kvs, dtype, d, G, lens, wide):
+    c = Cache(kvs, 1, len(lens), G, d, lens, dtype, seed=3, logn_scale=3.0, wide=wide)
     q = c.random(1, len(lens) * G, d, scale=2.0)
     c.check(q, c.step(q))
     kn, vn = c.random(1, len(lens), d), c.random(1, len(lens), d)
@@ -379,8 +393,8 @@ def test_decode_of_many_short_units(kvs, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_decode_steps_cross_a_page(kvs, dtype):
-    c = Cache(kvs, 1, 4, 4, 128, [0, 30, 31, 61], dtype, seed=5, room=5)
+def test_decode_steps_cross_a_page(kvs, dtype, wide):
+    c = Cache(kvs, 1, 4, 4, 128, [0, 30, 31, 61], dtype, seed=5, room=5, wide=wide)
     for _ in range(5):
         q, kn, vn = c.random(1, 16, 128), c.random(1, 4, 128), c.random(1, 4, 128)
         c.check(q, c.step(q, kn, vn), kn, vn)
@@ -391,8 +405,8 @@ def test_decode_steps_cross_a_page(kvs, dtype):
 @pytest.mark.parametrize("qs,ks,vs,ls", [(1, 1, 1e-4, 1), (1, 1, 1e-6, 1), (1, 1, 300., 1), (1, 1, 6e4, 1),
                                          (1e-5, 1, 1, 1), (1e4, 1e-3, 1, 1), (8, 4, 1, 1), (1, 1e-6, 1, 1),
                                          (1e-3, 2e3, 1, 40.)])
-def test_decode_over_the_range_of_values(kvs, dtype, qs, ks, vs, ls):
-    c = Cache(kvs, 1, 3, 4, 128, [300, 33, 1], dtype, seed=8, k_scale=ks, v_scale=vs, logn_scale=ls)
+def test_decode_over_the_range_of_values(kvs, dtype, qs, ks, vs, ls, wide):
+    c = Cache(kvs, 1, 3, 4, 128, [300, 33, 1], dtype, seed=8, k_scale=ks, v_scale=vs, logn_scale=ls, wide=wide)
     q = c.random(1, 12, 128, scale=qs)
     q[0, 5] = 0
     q[0, 6, 1:] = 0
@@ -400,10 +414,10 @@ def test_decode_over_the_range_of_values(kvs, dtype, qs, ks, vs, ls):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_decode_with_masked_rows(kvs, dtype):
+def test_decode_with_masked_rows(kvs, dtype, wide):
     """Log-counts of -inf or of the type's lowest value take rows out; a unit of nothing but
     -inf is zeros; the lowest value everywhere is a uniform shift."""
-    c = Cache(kvs, 1, 4, 4, 64, [70, 40, 65, 64], dtype, seed=9)
+    c = Cache(kvs, 1, 4, 4, 64, [70, 40, 65, 64], dtype, seed=9, wide=wide)
     low = float(np.finfo(np.float32).min)
     for u, t, x in [(0, t, -np.inf) for t in range(0, 70, 3)] + [(1, t, -np.inf) for t in range(40)] + \
             [(2, t, low / 2) for t in range(64)] + [(3, t, -np.inf) for t in range(32)]:
@@ -418,13 +432,15 @@ def test_decode_with_masked_rows(kvs, dtype):
         k, v, ln = ref.rows_of(c.pages_np, c.table_np[u], int(c.lens_np[u]), 64)
         keep = ln > low / 4
         want, size = ref.attend(q.double().cpu().numpy().reshape(4, 4, 64)[u], k[keep], v[keep], ln[keep])
-        bound = tolerance(dtype, q.double().cpu().numpy().reshape(4, 4, 64)[u], k[keep], v[keep], ln[keep], want, size)
+        scales = ref.value_scales(c.pages_np, c.table_np[u], int(c.lens_np[u]), 64)[keep]
+        bound = tolerance(dtype, q.double().cpu().numpy().reshape(4, 4, 64)[u], k[keep], v[keep], ln[keep], want,
+                          size, scales)
         assert np.all(np.abs(got[u] - want) <= bound)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_nan_stays_in_its_unit_or_query(kvs, dtype):
-    c = Cache(kvs, 1, 4, 2, 64, [50, 50, 50, 50], dtype, seed=10)
+def test_nan_stays_in_its_unit_or_query(kvs, dtype, wide):
+    c = Cache(kvs, 1, 4, 2, 64, [50, 50, 50, 50], dtype, seed=10, wide=wide)
     pg = c.pages_np[c.slot(1, 40) // PAGE]
     pg[34 * 64 + (1 * 32 + 40 % PAGE) * 2:][:2] = 255                 # value block 1 of one row of unit 1
     pg = c.pages_np[c.slot(3, 7) // PAGE]
@@ -440,8 +456,8 @@ def test_nan_stays_in_its_unit_or_query(kvs, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_full_units_and_bad_pages(kvs, dtype):
-    c = Cache(kvs, 1, 5, 2, 64, [64, 10, 32, 40, 40], dtype, seed=11, room=0)
+def test_full_units_and_bad_pages(kvs, dtype, wide):
+    c = Cache(kvs, 1, 5, 2, 64, [64, 10, 32, 40, 40], dtype, seed=11, room=0, wide=wide)
     c.table_np[0, 2:] = -1                                   # full: no page for row 64
     c.table_np[2, 1:] = -1
     c.table_np[4, 1] = len(c.pages_np)                       # past the pool: rows 32.. are skipped
@@ -454,16 +470,16 @@ def test_full_units_and_bad_pages(kvs, dtype):
     assert kvs.device_flags(c.ws, clear=True) == kvs.FLAG_OUT_CAPACITY | kvs.FLAG_BAD_PAGE
     assert c.lens.tolist() == [64, 11, 32, 41, 40]
     # lengths out of range: zeros, and the length stays
-    c.lens.copy_(i32([-3, 11, 33 * PAGE, 41, 0]))
+    c.lens.copy_(i32([-3, 11, 32 * c.table.shape[1] + 1, 41, 0]))
     out = c.step(q, kn, vn)
     assert not out[0, :2].any() and not out[0, 4:6].any() and out[0, 2:4].any()
     assert kvs.device_flags(c.ws, clear=True) == kvs.FLAG_BAD_LENGTH
-    assert c.lens.tolist() == [-3, 12, 33 * PAGE, 42, 1]
+    assert c.lens.tolist() == [-3, 12, 32 * c.table.shape[1] + 1, 42, 1]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_units_share_pages_that_none_appends_to(kvs, dtype):
-    c = Cache(kvs, 1, 2, 2, 128, [64, 70], dtype, seed=12)
+def test_units_share_pages_that_none_appends_to(kvs, dtype, wide):
+    c = Cache(kvs, 1, 2, 2, 128, [64, 70], dtype, seed=12, wide=wide)
     c.table_np[0, :2] = c.table_np[1, :2]
     c.to_device()
     q, kn, vn = c.random(1, 4, 128), c.random(1, 2, 128), c.random(1, 2, 128)
@@ -472,17 +488,17 @@ def test_units_share_pages_that_none_appends_to(kvs, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
-def test_the_same_call_gives_the_same_bits(kvs, dtype):
-    c = Cache(kvs, 1, 3, 4, 128, [4000, 1, 333], dtype, seed=13)
+def test_the_same_call_gives_the_same_bits(kvs, dtype, wide):
+    c = Cache(kvs, 1, 3, 4, 128, [4000, 1, 333], dtype, seed=13, wide=wide)
     q = c.random(1, 12, 128)
     first = c.step(q)
     for _ in range(20):
         assert torch.equal(c.step(q), first)
 
 
-def test_captured_steps_replay_like_eager_ones(kvs):
-    eager = Cache(kvs, 1, 4, 4, 128, [500, 0, 31, 64], torch.bfloat16, seed=14, room=8)
-    graph = Cache(kvs, 1, 4, 4, 128, [500, 0, 31, 64], torch.bfloat16, seed=14, room=8)
+def test_captured_steps_replay_like_eager_ones(kvs, wide):
+    eager = Cache(kvs, 1, 4, 4, 128, [500, 0, 31, 64], torch.bfloat16, seed=14, room=8, wide=wide)
+    graph = Cache(kvs, 1, 4, 4, 128, [500, 0, 31, 64], torch.bfloat16, seed=14, room=8, wide=wide)
     q, kn, vn = eager.random(1, 16, 128), eager.random(1, 4, 128), eager.random(1, 4, 128)
     lens0, pages0 = graph.lens.clone(), graph.pages.clone()
     out = torch.empty_like(q)
@@ -508,7 +524,7 @@ def test_captured_steps_replay_like_eager_ones(kvs):
 
 def test_two_streams_with_a_workspace_each(kvs):
     a = Cache(kvs, 1, 4, 4, 128, [3000, 5, 70, 1000], torch.bfloat16, seed=15)
-    b = Cache(kvs, 2, 2, 4, 128, [10, 2900, 0, 64], torch.bfloat16, seed=16)
+    b = Cache(kvs, 2, 2, 4, 128, [10, 2900, 0, 64], torch.bfloat16, seed=16, wide=5000)
     qa, qb = a.random(1, 16, 128), b.random(2, 8, 128)
     want_a, want_b = a.step(qa), b.step(qb)
     torch.cuda.synchronize()
