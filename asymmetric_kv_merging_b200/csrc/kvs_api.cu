@@ -479,7 +479,7 @@ kvs_status kvs_page_decode_attn(const kvs_cache_desc* desc, const void* q,
       !aligned(v_new, eb))
     return KVS_ERR_INVALID_ARG;
   const size_t units = (size_t)desc->B * desc->H_kv;
-  if (units * ((size_t)pool->max_pages + 1) > INT32_MAX) return KVS_ERR_INVALID_ARG;   // page numbering
+  if (units * ((size_t)pool->max_pages + 64) > INT32_MAX) return KVS_ERR_INVALID_ARG;   // page numbering
   const size_t qbytes = (size_t)desc->B * desc->H_q * desc->d * eb, nbytes = units * desc->d * eb;
   // what the call writes (the pages, the lengths and the output) must not overlap the rest
   const Range outs[] = {{(const char*)out, qbytes},

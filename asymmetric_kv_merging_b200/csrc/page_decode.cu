@@ -64,8 +64,10 @@ struct PageClusterShape {
 
 static bool use_cluster(int C, int max_pages) { return C >= 8 && max_pages <= 128 * C; }
 
-// Pages of a unit in the numbering: an empty one has one, so that a CTA finishes it.
-__device__ __forceinline__ int unit_span(int L) { return L > 0 ? pages_of(L) : 1; }
+// Places of a unit in the numbering: its pages, and some for the work at its end (an empty unit
+// has a place, so that a CTA finishes it).
+constexpr int kUnitPages = 8;
+__device__ __forceinline__ int unit_span(int L) { return pages_of(L) + kUnitPages; }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
@@ -172,8 +174,9 @@ struct PageWarp {
 // query heads in the N = 8 columns, as in the bf16 cache's decode (S^T = K Q^T, O^T = V^T P^T).
 //
 // The codes are never converted. A 4-bit code u in bits 0-3 or 4-7 of a 16-bit half IS the
-// subnormal half u 2^-24 or 16 u 2^-24, which the MMA multiplies exactly; so one AND makes an A
-// register out of a word of codes. The offset of 8 and the factors are put right outside:
+// subnormal half u 2^-24 or 16 u 2^-24, which the MMA multiplies exactly (and a byte of two codes
+// the sum of the two); so one AND or byte permutation makes an A register out of a word of codes.
+// The offset of 8 and the factors are put right outside:
 //   K: a_b = 2^-24 sum_c u q' over a block of 32 channels, x = sum_b scale_b (a_b - 8 2^-24 sum_c q').
 //      q' is the query times a power of two that puts its largest element into [2^14, 2^15): exact
 //      in half, as are the 1/16 of the channels in bits 4-7, down to 2^-28 of the largest
@@ -182,10 +185,15 @@ struct PageWarp {
 //   V: the block's scale goes onto the weights (B), w = half(half(p) scale), and
 //      sum_t (u - 8) scale p = sum_t u w - 8 sum_t scale p. The second sum is one MMA for all
 //      blocks, with the scales as A and the weights half(p) as B; it does not see the rounding
-//      of w, which therefore counts on |u| <= 15 instead of |u - 8| <= 7.
+//      of w, which therefore counts on |u| <= 15 instead of |u - 8| <= 7. Of two channels in a
+//      byte one is summed alone and the other as u + 16 u'; the difference is taken at the end.
 // p and w are rounded to half (2^-11 each); the reference m keeps p scale <= 2^15 and the largest
 // p at 2^7 (over scales above 1) or more when it was set, so weights down to 2^-21 of the largest
 // stay normal halves, and below that the error is at most 2^-25 / 2^7 of it.
+// The reference before the first row: below every logit, and finite, so that masked rows (-inf)
+// have a weight of 0 against it.
+constexpr float kNoRef = -1e30f;
+
 template <int D, int G>
 struct PageWarp<bf16, D, G> {
   using P = PageLayout<D>;
@@ -195,7 +203,7 @@ struct PageWarp<bf16, D, G> {
   uint32_t cb[2];              // B of the offset: -8 2^-24 sum q' of the blocks, in three half parts
   float f0, f1;                // logit (log2) per unit of the scaled accumulators
   float m0, m1, l0, l1;
-  float O[NB][2][4];           // rows: channels 4 g, 4 g + 1 | 4 g + 2, 4 g + 3 of block b
+  float O[NB][2][4];           // sums of u w, of channels 4 g (+ 2) and of 4 g + 1 (+ 3) times 16 plus it
   float off[4];                // row b: sum_t p scale of block b
   uint32_t poison;             // bit b: block b of some row reads as NaN
 
@@ -264,14 +272,14 @@ struct PageWarp<bf16, D, G> {
     }
     f0 = __shfl_sync(0xffffffffu, f, t * 8);
     f1 = __shfl_sync(0xffffffffu, f, t * 8 + 4);
-    m0 = m1 = -INFINITY;
+    m0 = m1 = kNoRef;
     l0 = l1 = 0.f;
     off[0] = off[1] = off[2] = off[3] = 0.f;
     poison = 0u;
   }
 
   __device__ __forceinline__ void take(unsigned char* pg, int nval, int lane) {
-    constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
+    constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u, BOTH = LO | HI;
     const int g = lane >> 2, t = lane & 3;
     if (nval < kPageRows) {
       // the page's other rows may hold anything: their weights are 0, so no scale may be NaN
@@ -364,8 +372,7 @@ struct PageWarp<bf16, D, G> {
         h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
       }
       const float n0 = h0 > lim0 ? h0 + (ev - 7.f) : m0, n1 = h1 > lim1 ? h1 + (ev - 7.f) : m1;
-      // factors of the old reference (0 when there was none: l and O are still 0)
-      const float e0 = n0 == m0 ? 1.f : ex2_ftz(m0 - n0), e1 = n1 == m1 ? 1.f : ex2_ftz(m1 - n1);
+      const float e0 = ex2_ftz(m0 - n0), e1 = ex2_ftz(m1 - n1);
       l0 *= e0;
       l1 *= e1;
 #pragma unroll
@@ -378,12 +385,11 @@ struct PageWarp<bf16, D, G> {
       m0 = n0;
       m1 = n1;
     }
-    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
     __half2 pb[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float p0 = ex2_ftz(x[i][0] - b0), p1 = ex2_ftz(x[i][1] - b1);
-      const float p2 = ex2_ftz(x[i][2] - b0), p3 = ex2_ftz(x[i][3] - b1);
+      const float p0 = ex2_ftz(x[i][0] - m0), p1 = ex2_ftz(x[i][1] - m1);
+      const float p2 = ex2_ftz(x[i][2] - m0), p3 = ex2_ftz(x[i][3] - m1);
       l0 += p0 + p2;
       l1 += p1 + p3;
       const __half2 u = __floats2half2_rn(p0, p1), v = __floats2half2_rn(p2, p3);
@@ -407,10 +413,10 @@ struct PageWarp<bf16, D, G> {
         const uint32_t va = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r, g));
         const uint32_t vb = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r + 8, g));
         float(&X)[4] = O[b][0];
-        mma_f16_16816(X, va & LO, va & HI, vb & LO, vb & HI, w0, w1, X[0], X[1], X[2], X[3]);
-        const uint32_t ua = va >> 8, ub = vb >> 8;
+        mma_f16_16816(X, va & LO, va & BOTH, vb & LO, vb & BOTH, w0, w1, X[0], X[1], X[2], X[3]);
+        const uint32_t ua = __byte_perm(va, 0u, 0x4341), ub = __byte_perm(vb, 0u, 0x4341);
         float(&Y)[4] = O[b][1];
-        mma_f16_16816(Y, ua & LO, ua & HI, ub & LO, ub & HI, w0, w1, Y[0], Y[1], Y[2], Y[3]);
+        mma_f16_16816(Y, ua & LO, ua, ub & LO, ub, w0, w1, Y[0], Y[1], Y[2], Y[3]);
       }
     }
   }
@@ -431,12 +437,12 @@ struct PageWarp<bf16, D, G> {
       const float(&X)[4] = O[b][0], (&Y)[4] = O[b][1];
       if (2 * t < G)
         *reinterpret_cast<float4*>(sa + 2 * t * D + b * 32 + g * 4) =
-            make_float4(fmaf(X[0], kUp, -z0), fmaf(X[2], kUp / 16, -z0), fmaf(Y[0], kUp, -z0),
-                        fmaf(Y[2], kUp / 16, -z0));
+            make_float4(fmaf(X[0], kUp, -z0), fmaf(X[2] - X[0], kUp / 16, -z0), fmaf(Y[0], kUp, -z0),
+                        fmaf(Y[2] - Y[0], kUp / 16, -z0));
       if (2 * t + 1 < G)
         *reinterpret_cast<float4*>(sa + (2 * t + 1) * D + b * 32 + g * 4) =
-            make_float4(fmaf(X[1], kUp, -z1), fmaf(X[3], kUp / 16, -z1), fmaf(Y[1], kUp, -z1),
-                        fmaf(Y[3], kUp / 16, -z1));
+            make_float4(fmaf(X[1], kUp, -z1), fmaf(X[3] - X[1], kUp / 16, -z1), fmaf(Y[1], kUp, -z1),
+                        fmaf(Y[3] - Y[1], kUp / 16, -z1));
     }
     if (g == 0) {
       if (2 * t < G) {
@@ -460,7 +466,8 @@ struct PageRing {
   unsigned char* pages;
   unsigned char* ring;
   uint64_t* full;
-  uint32_t list, next;
+  uint32_t list, next;           // the list that page k + ST is on, and the one after it
+  uint32_t due[ST];              // entries of the pages from k on
   int k, stage;
   uint32_t phase;                // bit s: parity of stage s
 
@@ -476,8 +483,7 @@ struct PageRing {
     pages = pages_;
     ring = ring_;
     full = full_;
-    next = first;
-    list = 0u;
+    list = first;
     k = stage = 0;
     phase = 0u;
     if (lane == 0) {
@@ -486,7 +492,10 @@ struct PageRing {
     }
     __syncwarp();
 #pragma unroll
-    for (int s = 0; s < ST; ++s) issue(s, __shfl_sync(0xffffffffu, next, s), lane);
+    for (int s = 0; s < ST; ++s) {
+      due[s] = __shfl_sync(0xffffffffu, list, s);
+      issue(s, due[s], lane);
+    }
   }
   // Hands the pages up to (not including) page `kend` to take(page in shared memory, rows).
   // False when a copy did not arrive: the warp's other copies have had their bound by then, and
@@ -494,25 +503,32 @@ struct PageRing {
   template <typename Fill, typename Take>
   __device__ __forceinline__ bool run(int kend, int lane, Fill&& fill, Take&& take) {
     for (; k < kend; ++k) {
-      if ((k & 31) == 0) {
-        list = next;
-        next = fill();
-      }
-      const uint32_t cur = __shfl_sync(0xffffffffu, list, k & 31);
+      const uint32_t cur = due[0];
       if (cur != 0u) {
         if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase >> stage & 1u))) {
+#pragma unroll
           for (int i = 0; i < ST; ++i) {
-            const uint32_t e = __shfl_sync(0xffffffffu, (k & 31) + i < 32 ? list : next, (k + i) & 31);
             const int s = (stage + i) % ST;
-            if (e != 0u) mbar_wait(&full[s], phase >> s & 1u);
+            if (due[i] != 0u) mbar_wait(&full[s], phase >> s & 1u);
+            due[i] = 0u;
           }
+          list = next = 0u;
           return false;
         }
         phase ^= 1u << stage;
         take(ring + stage * P::kBytes, (int)(cur & 63u));
         __syncwarp();
       }
-      issue(stage, __shfl_sync(0xffffffffu, (k & 31) + ST < 32 ? list : next, (k + ST) & 31), lane);
+      const int ahead = (k + ST) & 31;
+      if (k == 0) next = fill();
+      if (ahead == 0) {
+        list = next;
+        next = fill();
+      }
+#pragma unroll
+      for (int i = 0; i + 1 < ST; ++i) due[i] = due[i + 1];
+      due[ST - 1] = __shfl_sync(0xffffffffu, list, ahead);
+      issue(stage, due[ST - 1], lane);
       stage = stage + 1 == ST ? 0 : stage + 1;
     }
     return true;
@@ -753,7 +769,6 @@ page_decode_kernel(const PageArgs<T> a) {
       if (!pr.run((seg_end - f0 - warp + NW - 1) / NW, lane, fill,
                   [&](unsigned char* pg, int n) { pw.take(pg, n, lane); })) {
         set_flag(a.flags, KVS_FLAG_TIMEOUT);
-        pr.next = pr.list = 0u;
         lf = f1;
       }
       if (seg_end < f1) pw.load(a.q + (size_t)(u + 1) * G * D, lane);
@@ -805,16 +820,33 @@ page_decode_kernel(const PageArgs<T> a) {
       const float* rows = a.part + (size_t)sp.y * 2 * G * RS;
       auto row_of = [&](int s) { return rows + (2 * s + (s == 0 ? 1 : 0)) * G * RS; };
       float* fac = s_acc;                          // [G][np]
+      float4 v[kBatch];
+      auto load_batch = [&](int s0) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+          if (s0 + j * NGRP < np)
+            v[j] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + j * NGRP) + g * RS + c));
+      };
+      load_batch(grp);                             // with the factors' loads: one round trip for both
       if (warp < G) {
-        float M = -INFINITY;
-        for (int s = lane; s < np; s += 32) M = fmaxf(M, __ldcg(row_of(s) + warp * RS + D));
+        constexpr int kPer = (kPageDecodeCtas + 31) / 32;
+        float2 ml[kPer];
+        float M = -INFINITY, Ls = 0.f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int s = lane + j * 32;
+          ml[j] = make_float2(-INFINITY, 0.f);
+          if (j * 32 < np && s < np)
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(row_of(s) + warp * RS + D));
+          M = fmaxf(M, ml[j].x);
+        }
         M = warp_max(M);
-        float Ls = 0.f;
-        for (int s = lane; s < np; s += 32) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(row_of(s) + warp * RS + D));
-          const float f = part_weight(ml.x, ml.y, M);
-          Ls = fmaf(ml.y, f, Ls);
-          fac[warp * np + s] = f;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          const int s = lane + j * 32;
+          const float f = part_weight(ml[j].x, ml[j].y, M);
+          Ls = fmaf(ml[j].y, f, Ls);
+          if (s < np) fac[warp * np + s] = f;
         }
         Ls = warp_sum(Ls);
         if (lane == 0) {
@@ -825,11 +857,7 @@ page_decode_kernel(const PageArgs<T> a) {
       __syncthreads();
       float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int s0 = grp; s0 < np; s0 += kBatch * NGRP) {
-        float4 v[kBatch];
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-          if (s0 + j * NGRP < np)
-            v[j] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + j * NGRP) + g * RS + c));
+        if (s0 != grp) load_batch(s0);
 #pragma unroll
         for (int j = 0; j < kBatch; ++j)
           if (s0 + j * NGRP < np) {

@@ -419,7 +419,7 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * (KVS_FLAG_BAD_PAGE). T_cap of desc is not used. Two units may share a page that neither
  * appends to.
  * In:  q [B,H_q,d]; pool; len [B*H_kv], 0 <= len <= 32 max_pages;
- *      B * H_kv * (max_pages + 1) < 2^31.
+ *      B * H_kv * (max_pages + 64) < 2^31.
  * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
  * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes; its counters must be zero at
  * the first call (each call leaves them zero). Make the first call for a device outside any
