@@ -289,102 +289,83 @@ struct PageWarp<bf16, D, G> {
       fence_proxy_async_smem();      // the stage's next copy comes after these stores
       __syncwarp();
     }
+    // the two groups of 16 rows side by side: each step's MMAs are independent of one another
+    __half2 sa[2][NB / 2], sb[2][NB / 2];        // K scales of rows r and r + 8
     float x[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i * 16 + g;
-      __half2 sa[NB / 2], sb[NB / 2];            // K scales of rows r and r + 8
       if constexpr (NB == 4) {
         const uint2 u = *reinterpret_cast<const uint2*>(pg + P::k_scale(0, r));
         const uint2 v = *reinterpret_cast<const uint2*>(pg + P::k_scale(0, r + 8));
-        sa[0] = as_half2(u.x); sa[1] = as_half2(u.y);
-        sb[0] = as_half2(v.x); sb[1] = as_half2(v.y);
+        sa[i][0] = as_half2(u.x); sa[i][1] = as_half2(u.y);
+        sb[i][0] = as_half2(v.x); sb[i][1] = as_half2(v.y);
       } else {
-        sa[0] = *reinterpret_cast<const __half2*>(pg + P::k_scale(0, r));
-        sb[0] = *reinterpret_cast<const __half2*>(pg + P::k_scale(0, r + 8));
+        sa[i][0] = *reinterpret_cast<const __half2*>(pg + P::k_scale(0, r));
+        sb[i][0] = *reinterpret_cast<const __half2*>(pg + P::k_scale(0, r + 8));
       }
-      const uint32_t za = as_u32(t & 1 ? sa[NB / 2 - 1] : sa[0]), zb = as_u32(t & 1 ? sb[NB / 2 - 1] : sb[0]);
-      float y[4];
-      mma_f16_16816(y, za, zb, za, zb, cb[0], cb[1], 0.f, 0.f, 0.f, 0.f);
+      const uint32_t za = as_u32(t & 1 ? sa[i][NB / 2 - 1] : sa[i][0]);
+      const uint32_t zb = as_u32(t & 1 ? sb[i][NB / 2 - 1] : sb[i][0]);
+      mma_f16_16816(x[i], za, zb, za, zb, cb[0], cb[1], 0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint32_t wa = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, r) + t * 4);
-        const uint32_t wb = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, r + 8) + t * 4);
-        float a[4];
-        mma_f16_16816(a, wa & LO, wb & LO, wa & HI, wb & HI, qb[2 * b][0], qb[2 * b][1], 0.f, 0.f,
-                      0.f, 0.f);
-        const uint32_t ua = wa >> 8, ub = wb >> 8;
-        mma_f16_16816(a, ua & LO, ub & LO, ua & HI, ub & HI, qb[2 * b + 1][0], qb[2 * b + 1][1],
-                      a[0], a[1], a[2], a[3]);
-        const float s = b & 1 ? __high2float(sa[b / 2]) : __low2float(sa[b / 2]);
-        const float z = b & 1 ? __high2float(sb[b / 2]) : __low2float(sb[b / 2]);
-        y[0] = fmaf(s, a[0], y[0]);
-        y[1] = fmaf(s, a[1], y[1]);
-        y[2] = fmaf(z, a[2], y[2]);
-        y[3] = fmaf(z, a[3], y[3]);
+    for (int b = 0; b < NB; ++b) {
+      uint32_t wa[2], wb[2];
+      float a[2][4];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        wa[i] = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, i * 16 + g) + t * 4);
+        wb[i] = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, i * 16 + g + 8) + t * 4);
       }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        mma_f16_16816(a[i], wa[i] & LO, wb[i] & LO, wa[i] & HI, wb[i] & HI, qb[2 * b][0],
+                      qb[2 * b][1], 0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t ua = wa[i] >> 8, ub = wb[i] >> 8;
+        mma_f16_16816(a[i], ua & LO, ub & LO, ua & HI, ub & HI, qb[2 * b + 1][0], qb[2 * b + 1][1],
+                      a[i][0], a[i][1], a[i][2], a[i][3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float s = b & 1 ? __high2float(sa[i][b / 2]) : __low2float(sa[i][b / 2]);
+        const float z = b & 1 ? __high2float(sb[i][b / 2]) : __low2float(sb[i][b / 2]);
+        x[i][0] = fmaf(s, a[i][0], x[i][0]);
+        x[i][1] = fmaf(s, a[i][1], x[i][1]);
+        x[i][2] = fmaf(z, a[i][2], x[i][2]);
+        x[i][3] = fmaf(z, a[i][3], x[i][3]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = i * 16 + g;
       const float na = *reinterpret_cast<const float*>(pg + P::logn(r)) * kLog2e;
       const float nb = *reinterpret_cast<const float*>(pg + P::logn(r + 8)) * kLog2e;
-      x[i][0] = fmaf(y[0], f0, na);
-      x[i][1] = fmaf(y[1], f1, na);
-      x[i][2] = fmaf(y[2], f0, nb);
-      x[i][3] = fmaf(y[3], f1, nb);
+      x[i][0] = fmaf(x[i][0], f0, na);
+      x[i][1] = fmaf(x[i][1], f1, na);
+      x[i][2] = fmaf(x[i][2], f0, nb);
+      x[i][3] = fmaf(x[i][3], f1, nb);
       if (nval < kPageRows) {
         if (r >= nval) x[i][0] = x[i][1] = -INFINITY;
         if (r + 8 >= nval) x[i][2] = x[i][3] = -INFINITY;
       }
     }
-    // 2^ev > every V scale of the page (at least 1): p 2^ev stays below 2^15
-    uint32_t smax;
+    // The reference of a column moves only when a weight would pass 2^15, to where the largest is
+    // 2^7: after the first pages that is rare. Scales above 1 take the same path, since p scale
+    // has to stay below 2^15 too, and so do NaN scales (adding 0x43ff carries a half above 1.0
+    // into its sign bit).
+    uint32_t big;
     if constexpr (NB == 4) {
       const uint2 w = *reinterpret_cast<const uint2*>(pg + P::kVs + lane * 8);
-      smax = __vmaxu2(w.x, w.y);
+      big = (w.x + 0x43ff43ffu) | (w.y + 0x43ff43ffu);
     } else {
-      smax = *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4);
+      big = *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4) + 0x43ff43ffu;
     }
-    smax = __reduce_max_sync(0xffffffffu, max(smax & 0xffffu, smax >> 16));
-    const float ev = (float)max(0, (int)(smax >> 10) - 14);
-    if (smax > 0x7c00u) {
-      // Blocks that read as NaN: 0 x NaN would reach the other blocks through the shared sum of
-      // weights, so the scales go and end() puts the NaN where it belongs.
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint16_t* sp = reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane));
-        const bool bad = *sp > 0x7c00u;
-        if (bad) *sp = 0;
-        if (__any_sync(0xffffffffu, bad)) poison |= 1u << b;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-    }
-    // The reference of a column moves only when a weight would pass 2^15, to where the largest is
-    // 2^7: after the first pages that is rare, and so are the maxima over the rows (the 8 lanes
-    // sharing t) and the rescale.
-    const float lim0 = m0 + (15.f - ev), lim1 = m1 + (15.f - ev);
-    const bool up = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2])) > lim0 ||
-                    fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3])) > lim1;
-    if (__any_sync(0xffffffffu, up)) {
-      float h0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
-      float h1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
-#pragma unroll
-      for (int o = 4; o < 32; o <<= 1) {
-        h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));
-        h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
-      }
-      const float n0 = h0 > lim0 ? h0 + (ev - 7.f) : m0, n1 = h1 > lim1 ? h1 + (ev - 7.f) : m1;
-      const float e0 = ex2_ftz(m0 - n0), e1 = ex2_ftz(m1 - n1);
-      l0 *= e0;
-      l1 *= e1;
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          O[b][j][0] *= e0; O[b][j][1] *= e1; O[b][j][2] *= e0; O[b][j][3] *= e1;
-        }
-      off[0] *= e0; off[1] *= e1; off[2] *= e0; off[3] *= e1;
-      m0 = n0;
-      m1 = n1;
-    }
+    const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
+    const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
+    if (__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > m0 + 15.f || h1 > m1 + 15.f))
+      move_reference(pg, h0, h1, lane);
     __half2 pb[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -419,6 +400,48 @@ struct PageWarp<bf16, D, G> {
         mma_f16_16816(Y, ua & LO, ua, ub & LO, ub, w0, w1, Y[0], Y[1], Y[2], Y[3]);
       }
     }
+  }
+
+  // The reference for a page whose largest logits in this lane's columns and rows are h0, h1, and
+  // its blocks that read as NaN.
+  __device__ __forceinline__ void move_reference(unsigned char* pg, float h0, float h1, int lane) {
+    uint32_t smax = 0, nan = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      uint16_t* sp = reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane));
+      const uint32_t v = *sp;
+      if (__any_sync(0xffffffffu, v > 0x7c00u)) nan |= 1u << b;
+      if (v > 0x7c00u) *sp = 0;
+      else smax = max(smax, v);
+    }
+    if (nan != 0u) {
+      // 0 x NaN would reach the other blocks through the shared sum of weights, so those scales
+      // go, and end() puts the NaN where it belongs
+      poison |= nan;
+      fence_proxy_async_smem();      // the stage's next copy comes after these stores
+      __syncwarp();
+    }
+    // 2^ev > every V scale of the page (at least 1)
+    const float ev = (float)max(0, (int)(__reduce_max_sync(0xffffffffu, smax) >> 10) - 14);
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {               // the 8 lanes sharing t
+      h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));
+      h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
+    }
+    const float n0 = h0 + ev > m0 + 15.f ? h0 + (ev - 7.f) : m0;
+    const float n1 = h1 + ev > m1 + 15.f ? h1 + (ev - 7.f) : m1;
+    const float e0 = ex2_ftz(m0 - n0), e1 = ex2_ftz(m1 - n1);
+    l0 *= e0;
+    l1 *= e1;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        O[b][j][0] *= e0; O[b][j][1] *= e1; O[b][j][2] *= e0; O[b][j][3] *= e1;
+      }
+    off[0] *= e0; off[1] *= e1; off[2] *= e0; off[3] *= e1;
+    m0 = n0;
+    m1 = n1;
   }
 
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
