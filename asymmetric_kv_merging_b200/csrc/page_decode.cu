@@ -306,7 +306,7 @@ struct PageWarp<bf16, D, G> {
       }
       const uint32_t za = as_u32(t & 1 ? sa[i][NB / 2 - 1] : sa[i][0]);
       const uint32_t zb = as_u32(t & 1 ? sb[i][NB / 2 - 1] : sb[i][0]);
-      mma_f16_16816(x[i], za, zb, za, zb, cb[0], cb[1], 0.f, 0.f, 0.f, 0.f);
+      mma_f16_16816_zero(x[i], za, zb, za, zb, cb[0], cb[1]);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -319,13 +319,12 @@ struct PageWarp<bf16, D, G> {
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        mma_f16_16816(a[i], wa[i] & LO, wb[i] & LO, wa[i] & HI, wb[i] & HI, qb[2 * b][0],
-                      qb[2 * b][1], 0.f, 0.f, 0.f, 0.f);
+        mma_f16_16816_zero(a[i], wa[i] & LO, wb[i] & LO, wa[i] & HI, wb[i] & HI, qb[2 * b][0],
+                           qb[2 * b][1]);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t ua = wa[i] >> 8, ub = wb[i] >> 8;
-        mma_f16_16816(a[i], ua & LO, ub & LO, ua & HI, ub & HI, qb[2 * b + 1][0], qb[2 * b + 1][1],
-                      a[i][0], a[i][1], a[i][2], a[i][3]);
+        mma_f16_16816(a[i], ua & LO, ub & LO, ua & HI, ub & HI, qb[2 * b + 1][0], qb[2 * b + 1][1]);
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -385,8 +384,7 @@ struct PageWarp<bf16, D, G> {
       // row g of A: the scales of block g
       const uint32_t za = g < NB ? *reinterpret_cast<const uint32_t*>(pg + P::v_scale(g, r)) : 0u;
       const uint32_t zb = g < NB ? *reinterpret_cast<const uint32_t*>(pg + P::v_scale(g, r + 8)) : 0u;
-      mma_f16_16816(off, za, 0u, zb, 0u, as_u32(pb[i][0]), as_u32(pb[i][1]), off[0], off[1], off[2],
-                    off[3]);
+      mma_f16_16816(off, za, 0u, zb, 0u, as_u32(pb[i][0]), as_u32(pb[i][1]));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const uint32_t w0 = as_u32(__hmul2(pb[i][0], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r))));
@@ -394,10 +392,10 @@ struct PageWarp<bf16, D, G> {
         const uint32_t va = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r, g));
         const uint32_t vb = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r + 8, g));
         float(&X)[4] = O[b][0];
-        mma_f16_16816(X, va & LO, va & BOTH, vb & LO, vb & BOTH, w0, w1, X[0], X[1], X[2], X[3]);
+        mma_f16_16816(X, va & LO, va & BOTH, vb & LO, vb & BOTH, w0, w1);
         const uint32_t ua = __byte_perm(va, 0u, 0x4341), ub = __byte_perm(vb, 0u, 0x4341);
         float(&Y)[4] = O[b][1];
-        mma_f16_16816(Y, ua & LO, ua, ub & LO, ub, w0, w1, Y[0], Y[1], Y[2], Y[3]);
+        mma_f16_16816(Y, ua & LO, ua, ub & LO, ub, w0, w1);
       }
     }
   }
