@@ -86,6 +86,7 @@ struct PageWarp {
   const float (*qs)[D];
   float m[G], l[G], acc[G][4];
 
+  __device__ __forceinline__ void init(__half*, int) {}
   __device__ __forceinline__ void load(const T*, int) {}
   __device__ __forceinline__ void begin(const float (*qs_)[D], int) {
     qs = qs_;
@@ -184,8 +185,8 @@ struct PageWarp {
 //      B the blocks' sums of q' in three half parts (33 bits); it starts x.
 //   V: the block's scale goes onto the weights (B), w = half(half(p) scale), and
 //      sum_t (u - 8) scale p = sum_t u w - 8 sum_t scale p. The second sum is one MMA for all
-//      blocks, with the scales as A and the weights half(p) as B; it does not see the rounding
-//      of w, which therefore counts on |u| <= 15 instead of |u - 8| <= 7. Of two channels in a
+//      blocks, with the scales as A and the weights half(p) as B (and a row of ones, for the sum
+//      of the weights); it does not see the rounding of w, which therefore counts on |u| <= 15 instead of |u - 8| <= 7. Of two channels in a
 //      byte one is summed alone and the other as u + 16 u'; the difference is taken at the end.
 // p and w are rounded to half (2^-11 each); the reference m keeps p scale <= 2^15 and the largest
 // p at 2^7 (over scales above 1) or more when it was set, so weights down to 2^-21 of the largest
@@ -202,10 +203,19 @@ struct PageWarp<bf16, D, G> {
   uint32_t qb[2 * NB][2];      // B of S^T: [2 b + i], k slots (8 t + 2 i, + 4) and (8 t + 2 i + 1, + 5)
   uint32_t cb[2];              // B of the offset: -8 2^-24 sum q' of the blocks, in three half parts
   float f0, f1;                // logit (log2) per unit of the scaled accumulators
-  float m0, m1, l0, l1;
+  float m0, m1;                // the references (log2), and as the start of a logit's sums:
+  float r0, r1;                // -m / f (0 while there is none)
+  float lim0, lim1;            // a logit over the reference by more than this moves it
   float O[NB][2][4];           // sums of u w, of channels 4 g (+ 2) and of 4 g + 1 (+ 3) times 16 plus it
-  float off[4];                // row b: sum_t p scale of block b
+  float off[4];                // row b: sum_t p scale of block b; row 4: sum_t p
+  uint32_t ones;               // shared memory: 16 bytes of 1.0, 16 bytes of 0
   uint32_t poison;             // bit b: block b of some row reads as NaN
+
+  // `ones_`: 32 bytes of shared memory of this warp's own
+  __device__ __forceinline__ void init(__half* ones_, int lane) {
+    if (lane < 16) ones_[lane] = __float2half_rn(lane < 8 ? 1.f : 0.f);
+    ones = smem_u32(ones_);
+  }
 
   __device__ __forceinline__ void load(const bf16* q, int lane) {
     const int g = lane >> 2, t = lane & 3;
@@ -273,7 +283,8 @@ struct PageWarp<bf16, D, G> {
     f0 = __shfl_sync(0xffffffffu, f, t * 8);
     f1 = __shfl_sync(0xffffffffu, f, t * 8 + 4);
     m0 = m1 = kNoRef;
-    l0 = l1 = 0.f;
+    r0 = r1 = 0.f;
+    lim0 = lim1 = -INFINITY;
     off[0] = off[1] = off[2] = off[3] = 0.f;
     poison = 0u;
   }
@@ -282,10 +293,15 @@ struct PageWarp<bf16, D, G> {
     constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u, BOTH = LO | HI;
     const int g = lane >> 2, t = lane & 3;
     if (nval < kPageRows) {
-      // the page's other rows may hold anything: their weights are 0, so no scale may be NaN
-      if (lane >= nval)
+      // the page's other rows may hold anything: a logit of 0 - inf, and a weight of 0 for a value of 0
+      if (lane >= nval) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane)) = 0;
+        for (int b = 0; b < NB; ++b) {
+          *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, lane)) = 0;
+          *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane)) = 0;
+        }
+        *reinterpret_cast<float*>(pg + P::logn(lane)) = -INFINITY;
+      }
       fence_proxy_async_smem();      // the stage's next copy comes after these stores
       __syncwarp();
     }
@@ -306,17 +322,16 @@ struct PageWarp<bf16, D, G> {
       }
       const uint32_t za = as_u32(t & 1 ? sa[i][NB / 2 - 1] : sa[i][0]);
       const uint32_t zb = as_u32(t & 1 ? sb[i][NB / 2 - 1] : sb[i][0]);
-      mma_f16_16816_zero(x[i], za, zb, za, zb, cb[0], cb[1]);
+      x[i][0] = x[i][2] = r0;
+      x[i][1] = x[i][3] = r1;
+      mma_f16_16816(x[i], za, zb, za, zb, cb[0], cb[1]);
     }
+    const uint32_t base = smem_u32(pg);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      uint32_t wa[2], wb[2];
+      uint32_t wa[2], wb[2];                       // word t of rows g, g + 8, g + 16, g + 24
+      ldsm_x4(base + P::k_code(b, 0) + lane * 16, wa[0], wb[0], wa[1], wb[1]);
       float a[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        wa[i] = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, i * 16 + g) + t * 4);
-        wb[i] = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, i * 16 + g + 8) + t * 4);
-      }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         mma_f16_16816_zero(a[i], wa[i] & LO, wb[i] & LO, wa[i] & HI, wb[i] & HI, qb[2 * b][0],
@@ -345,10 +360,6 @@ struct PageWarp<bf16, D, G> {
       x[i][1] = fmaf(x[i][1], f1, na);
       x[i][2] = fmaf(x[i][2], f0, nb);
       x[i][3] = fmaf(x[i][3], f1, nb);
-      if (nval < kPageRows) {
-        if (r >= nval) x[i][0] = x[i][1] = -INFINITY;
-        if (r + 8 >= nval) x[i][2] = x[i][3] = -INFINITY;
-      }
     }
     // The reference of a column moves only when a weight would pass 2^15, to where the largest is
     // 2^7: after the first pages that is rare. Scales above 1 take the same path, since p scale
@@ -363,46 +374,55 @@ struct PageWarp<bf16, D, G> {
     }
     const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
     const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
-    if (__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > m0 + 15.f || h1 > m1 + 15.f))
-      move_reference(pg, h0, h1, lane);
+    if (__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > lim0 || h1 > lim1)) {
+      float2 up = move_reference(pg, h0, h1, lane);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i][0] -= up.x; x[i][1] -= up.y; x[i][2] -= up.x; x[i][3] -= up.y;
+      }
+    }
     __half2 pb[2][2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const float p0 = ex2_ftz(x[i][0] - m0), p1 = ex2_ftz(x[i][1] - m1);
-      const float p2 = ex2_ftz(x[i][2] - m0), p3 = ex2_ftz(x[i][3] - m1);
-      l0 += p0 + p2;
-      l1 += p1 + p3;
-      const __half2 u = __floats2half2_rn(p0, p1), v = __floats2half2_rn(p2, p3);
+      const __half2 u = __floats2half2_rn(ex2_ftz(x[i][0]), ex2_ftz(x[i][1]));
+      const __half2 v = __floats2half2_rn(ex2_ftz(x[i][2]), ex2_ftz(x[i][3]));
       const uint32_t ut = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&u));
       const uint32_t vt = movmatrix_trans(*reinterpret_cast<const uint32_t*>(&v));
       pb[i][0] = *reinterpret_cast<const __half2*>(&ut);
       pb[i][1] = *reinterpret_cast<const __half2*>(&vt);
     }
+    // V scales of row pairs t, t + 4, t + 8, t + 12 of every block: each matrix eight times the same
+    // 16 bytes. As A (`za`): row b the scales of block b, row 4 ones, so that the sums of weights
+    // come with the sums of scaled weights.
+    uint32_t sv[NB][4], za[4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+      ldsm_x4(base + P::v_scale(b, 0) + (lane >> 3) * 16, sv[b][0], sv[b][1], sv[b][2], sv[b][3]);
+    {
+      const int row = lane & 7;
+      ldsm_x4(row < NB ? base + P::kVs + row * 64 + (lane >> 3) * 16 : ones + (row == 4 ? 0u : 16u),
+              za[0], za[1], za[2], za[3]);
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i * 16 + 2 * t;
-      // row g of A: the scales of block g
-      const uint32_t za = g < NB ? *reinterpret_cast<const uint32_t*>(pg + P::v_scale(g, r)) : 0u;
-      const uint32_t zb = g < NB ? *reinterpret_cast<const uint32_t*>(pg + P::v_scale(g, r + 8)) : 0u;
-      mma_f16_16816(off, za, 0u, zb, 0u, as_u32(pb[i][0]), as_u32(pb[i][1]));
+      mma_f16_16816(off, za[2 * i], 0u, za[2 * i + 1], 0u, as_u32(pb[i][0]), as_u32(pb[i][1]));
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const uint32_t w0 = as_u32(__hmul2(pb[i][0], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r))));
-        const uint32_t w1 = as_u32(__hmul2(pb[i][1], *reinterpret_cast<const __half2*>(pg + P::v_scale(b, r + 8))));
+        const uint32_t w0 = as_u32(__hmul2(pb[i][0], as_half2(sv[b][2 * i])));
+        const uint32_t w1 = as_u32(__hmul2(pb[i][1], as_half2(sv[b][2 * i + 1])));
         const uint32_t va = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r, g));
         const uint32_t vb = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r + 8, g));
-        float(&X)[4] = O[b][0];
-        mma_f16_16816(X, va & LO, va & BOTH, vb & LO, vb & BOTH, w0, w1);
+        mma_f16_16816(O[b][0], va & LO, va & BOTH, vb & LO, vb & BOTH, w0, w1);
         const uint32_t ua = __byte_perm(va, 0u, 0x4341), ub = __byte_perm(vb, 0u, 0x4341);
-        float(&Y)[4] = O[b][1];
-        mma_f16_16816(Y, ua & LO, ua, ub & LO, ub, w0, w1);
+        mma_f16_16816(O[b][1], ua & LO, ua, ub & LO, ub, w0, w1);
       }
     }
   }
 
-  // The reference for a page whose largest logits in this lane's columns and rows are h0, h1, and
-  // its blocks that read as NaN.
-  __device__ __forceinline__ void move_reference(unsigned char* pg, float h0, float h1, int lane) {
+  // The references for a page whose largest logits over them in this lane's columns and rows are
+  // h0, h1 (returns by how much they moved), and its blocks that read as NaN.
+  __device__ __forceinline__ float2 move_reference(unsigned char* pg, float h0, float h1, int lane) {
     uint32_t smax = 0, nan = 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -426,11 +446,10 @@ struct PageWarp<bf16, D, G> {
       h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));
       h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
     }
-    const float n0 = h0 + ev > m0 + 15.f ? h0 + (ev - 7.f) : m0;
-    const float n1 = h1 + ev > m1 + 15.f ? h1 + (ev - 7.f) : m1;
-    const float e0 = ex2_ftz(m0 - n0), e1 = ex2_ftz(m1 - n1);
-    l0 *= e0;
-    l1 *= e1;
+    const float u0 = h0 + ev > lim0 ? h0 + (ev - 7.f) : 0.f;
+    const float u1 = h1 + ev > lim1 ? h1 + (ev - 7.f) : 0.f;
+    // (before there is a reference, O and off are 0 and u may be anything)
+    const float e0 = lim0 < 0.f ? 0.f : ex2_ftz(-u0), e1 = lim1 < 0.f ? 0.f : ex2_ftz(-u1);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -438,18 +457,23 @@ struct PageWarp<bf16, D, G> {
         O[b][j][0] *= e0; O[b][j][1] *= e1; O[b][j][2] *= e0; O[b][j][3] *= e1;
       }
     off[0] *= e0; off[1] *= e1; off[2] *= e0; off[3] *= e1;
-    m0 = n0;
-    m1 = n1;
+    if (h0 > -INFINITY) {                            // (the column has a row that counts)
+      m0 = lim0 < 0.f ? u0 : m0 + u0;
+      r0 = -m0 / f0;
+      lim0 = 15.f;
+    }
+    if (h1 > -INFINITY) {
+      m1 = lim1 < 0.f ? u1 : m1 + u1;
+      r1 = -m1 / f1;
+      lim1 = 15.f;
+    }
+    return make_float2(u0, u1);
   }
 
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
     const int g = lane >> 2, t = lane & 3;
     constexpr float kUp = 16777216.f;
-#pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      l0 += __shfl_xor_sync(0xffffffffu, l0, o);
-      l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-    }
+    const float l0 = __shfl_sync(0xffffffffu, off[0], 16 + t), l1 = __shfl_sync(0xffffffffu, off[1], 16 + t);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       float z0 = __shfl_sync(0xffffffffu, off[0], b * 4 + t) * 8.f;
@@ -669,6 +693,7 @@ page_decode_kernel(const PageArgs<T> a) {
   extern __shared__ __align__(128) unsigned char dsm[];
   float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
   __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
+  __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
   __shared__ float s_m[NW][G], s_l[NW][G], s_stat[G][2];
   // the new row's logits and page for the unit that began in an earlier CTA (0), the one that
   // goes on in a later one (1), and units that are whole here (2 and 3 in turn)
@@ -760,6 +785,7 @@ page_decode_kernel(const PageArgs<T> a) {
     // the queries ahead of the pages: behind 150 KB of copies per SM they would come
     // microseconds later
     PageWarp<T, D, G> pw;
+    pw.init(s_ones[warp], lane);
     pw.load(a.q + (size_t)cp.u * G * D, lane);
     PageRing<D, ST> pr;
     pr.start(a.pages, dsm + warp * ST * P::kBytes,
@@ -937,6 +963,7 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
   float* s_sum = reinterpret_cast<float*>(dsm + S::kRing + S::kAcc);        // [G][D], read by peers
   __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
+  __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
   __shared__ float s_m[NW][G], s_l[NW][G], s_new[G];
   __shared__ __align__(8) float s_ml[G][2];                                 // read by peers
 
@@ -948,6 +975,7 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   long long j = rank + (long long)C * (warp + NW * lane);      // this lane's page of list 0
   int id = j < a.max_pages ? a.table[(size_t)u * a.max_pages + j] : -1;
   PageWarp<T, D, G> pw;
+  pw.init(s_ones[warp], lane);
   pw.load(a.q + (size_t)u * G * D, lane);
   if (L != len && rank == 0 && tid == 0) set_flag(a.flags, KVS_FLAG_BAD_LENGTH);
   auto entry = [&]() -> uint32_t {

@@ -364,6 +364,11 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
       : "memory");
 }
 
+// Untiled bulk prefetch of `bytes` (a multiple of 16) at a 16-byte aligned address into L2.
+__device__ __forceinline__ void bulk_prefetch_l2(const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
+}
+
 // Order this thread's generic-proxy view of global memory before its later async-proxy
 // (bulk copy) accesses.
 __device__ __forceinline__ void fence_proxy_async_global() {

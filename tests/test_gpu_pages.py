@@ -6,10 +6,11 @@ that is derived, with A = sum_t p_t |v_t| and n rows:
         X = sum |q k| / sqrt(d) (+ |logn|), make the weights off by 2 (d + 6) 2^-24 X relative;
         n + 16 roundings of the sums and the exponential's 2^-22 add to that.
   bf16  in addition, with s the scale of a value's block and S = sum_t p_t s_t:
-        the weight is rounded to half, h(p), which both sums of  sum u w - 8 sum s h(p)  see: 2^-11 A;
+        the weight is rounded to half, h(p), which both sums of  sum u w - 8 sum s h(p)  see, and so
+        does the sum of the weights that divides them: 2^-11 (A + |out|);
         w = half(s h(p)) is seen by the first one only, where the code u is at most 15: 15 2^-11 S;
         weights (and w) below the half range are off by at most 2^-25 each, the largest p being at
-        least 2^7 over the largest scale above 1: n 2^-32 max(1, s) (|v| + 15 s), and the logit's
+        least 2^7 over the largest scale above 1: n 2^-32 max(1, s) (2 |v| + 15 s), and the logit's
         offset sum is held to 2^-33 of it; and the output is rounded to bf16, 2^-8 |out|.
 """
 
@@ -342,8 +343,8 @@ def tolerance(dtype, q, k, v, logn, want, size, scales=None):
     s = np.zeros_like(v)                            # the new row, if there is one, is not rounded
     s[:len(scales)] = np.repeat(scales, 32, 1)
     p = ref.weights(q, k, logn)
-    low = n * 2.0 ** -32 * max(1.0, float(s.max())) * (np.abs(v) + 15 * s).max(0)
-    return (rel + 2.0 ** -11) * size + 15 * 2.0 ** -11 * (p @ s) + low + 2.0 ** -8 * np.abs(want)
+    low = n * 2.0 ** -32 * max(1.0, float(s.max())) * (2 * np.abs(v) + 15 * s).max(0)
+    return rel * size + 2.0 ** -11 * (size + np.abs(want)) + 15 * 2.0 ** -11 * (p @ s) + low + 2.0 ** -8 * np.abs(want)
 
 
 EDGE = [0, 1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 100, 255, 256, 257]
