@@ -645,11 +645,14 @@ __device__ __forceinline__ void write_new_row(const PageArgs<T>& a, int u, int L
   using P = PageLayout<D>;
   if (warp >= 2) return;
   const T* src = (warp == 0 ? a.k_new : a.v_new) + (size_t)u * D;
-  float x[8];
+  float x[8];                    // element loads: these rows need not be 16-byte aligned
 #pragma unroll
   for (int c = 0; c < 8; ++c) x[c] = lane < D / 8 ? to_f32(src[lane * 8 + c]) : 0.f;
+  Raw8<float> raw;
+  raw.a = make_float4(x[0], x[1], x[2], x[3]);
+  raw.b = make_float4(x[4], x[5], x[6], x[7]);
   uint32_t sb;
-  const uint32_t w = quantise_lane<T>(x, sb);
+  const uint32_t w = quantise_lane<float>(raw, sb);
   if (lane >= D / 8) return;
   unsigned char* pg = a.pages + (size_t)id * P::kBytes;
   const int r = L % kPageRows, b = lane / 4, sub = lane % 4;

@@ -156,61 +156,82 @@ cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32
 // Rows to pages and back
 // ---------------------------------------------------------------------------
 
+// A warp takes 8 consecutive rows, lane l channels 8 (l mod 4) .. of row l / 4 of one block of 32
+// channels after another. Codes of consecutive slots are then whole 128-byte lines (8 rows of 16
+// bytes; 4 pairs of 32), the maximum of a block is two shuffles away, and a lane has all the
+// loads of its row (8 of 16 bytes at d = 128 in bf16) in flight together.
 constexpr int kRowThreads = 256;
+constexpr int kRowsPerWarp = 8;
+constexpr int kRowsPerBlock = kRowThreads / 32 * kRowsPerWarp;
 
-// Lane l of a warp holds 8 channels of row l / (D / 8) of the warp's rows (two at D = 128).
+// Whether the V codes of two neighbouring rows (lanes l and l ^ 4) share words: the rows' slots
+// are a pair of the page, in order.
+__device__ __forceinline__ bool paired(int slot, int lane) {
+  const int other = __shfl_xor_sync(0xffffffffu, slot, 4);
+  return slot >= 0 && other == (slot ^ 1) && (slot & 1) == ((lane >> 2) & 1);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads)
 page_store_kernel(const T* __restrict__ K, const T* __restrict__ V, const float* __restrict__ logn,
                   const int32_t* __restrict__ slots, long long n_rows,
                   unsigned char* __restrict__ pages, int n_slots, int32_t* flags) {
   using P = PageLayout<D>;
-  constexpr int LPR = D / 8, RPW = 32 / LPR;            // lanes per row, rows per warp step
-  const int lane = threadIdx.x & 31, c8 = lane % LPR, b = c8 / 4, sub = c8 % 4;
-  const long long nwarps = (long long)gridDim.x * (kRowThreads / 32);
-  for (long long r0 = ((long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32) * RPW;
-       r0 < n_rows; r0 += nwarps * RPW) {
-    const long long r = r0 + lane / LPR;
-    int slot = r < n_rows ? slots[r] : -1;
-    if (slot >= n_slots) {
-      if (c8 == 0) set_flag(flags, KVS_FLAG_BAD_PAGE);
-      slot = -1;
-    }
-    const bool live = slot >= 0;
-    float k[8], v[8];
-    if (live) {
-#pragma unroll
-      for (int i = 0; i < 8; i += Vec16<T>::n) {
-        load_vec_cs(K + r * D + c8 * 8 + i, k + i);
-        load_vec_cs(V + r * D + c8 * 8 + i, v + i);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) k[i] = v[i] = 0.f;
-    }
-    uint32_t ks, vs;
-    const uint32_t kw = quantise_lane<T>(k, ks), vw = quantise_lane<T>(v, vs);
-    // the neighbouring row of the pair: one word of V per lane when both rows land in one pair
-    const int other = __shfl_xor_sync(0xffffffffu, slot, LPR);
-    const uint32_t ow = __shfl_xor_sync(0xffffffffu, vw, LPR);
-    if (!live) continue;
-    unsigned char* pg = pages + (size_t)(slot / kPageRows) * P::kBytes;
-    const int row = slot % kPageRows;
-    *reinterpret_cast<uint32_t*>(pg + P::k_code(b, row) + sub * 4) = kw;
-    const bool odd = (lane / LPR) & 1;
-    if ((slot & 1) == (int)odd && other == (slot ^ 1)) {
-      const uint32_t w = odd ? __byte_perm(ow, vw, 0x7632) : __byte_perm(vw, ow, 0x5410);
-      *reinterpret_cast<uint32_t*>(pg + P::v_piece(b, row & ~1, sub * 2 + (odd ? 1 : 0))) = w;
-    } else {
-      *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, row, sub * 2)) = (uint16_t)vw;
-      *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, row, sub * 2 + 1)) = (uint16_t)(vw >> 16);
-    }
-    if (sub == 0) {
-      *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, row)) = (uint16_t)ks;
-      *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, row)) = (uint16_t)vs;
-    }
-    if (c8 == 0) *reinterpret_cast<float*>(pg + P::logn(row)) = logn ? logn[r] : 0.f;
+  constexpr int NB = P::nb;
+  const int lane = threadIdx.x & 31, sub = lane & 3;
+  const long long r = (long long)blockIdx.x * kRowsPerBlock + threadIdx.x / 4;
+  int slot = r < n_rows ? slots[r] : -1;
+  if (slot >= n_slots) {
+    if (sub == 0) set_flag(flags, KVS_FLAG_BAD_PAGE);
+    slot = -1;
   }
+  if (!__any_sync(0xffffffffu, slot >= 0)) return;
+  const bool live = slot >= 0;
+  Raw8<T> k[NB], v[NB];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (live) {
+      k[b].load(K + r * D + b * 32 + sub * 8);
+      v[b].load(V + r * D + b * 32 + sub * 8);
+    } else {
+      k[b].zero();
+      v[b].zero();
+    }
+  }
+  const float ln = live && logn && sub == 0 ? logn[r] : 0.f;
+  const bool pair = paired(slot, lane);
+  const int row = slot & (kPageRows - 1);
+  unsigned char* pg = pages + (size_t)(live ? slot / kPageRows : 0) * P::kBytes;
+  uint32_t ks[NB], vs = 0;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t kw = quantise_lane<T>(k[b], ks[b]);
+    uint32_t s;
+    const uint32_t vw = quantise_lane<T>(v[b], s);
+    if (sub == b) vs = s;
+    // of a pair, the first row's lane writes both rows' pieces of quad 2 sub, the second's of 2 sub + 1
+    const uint32_t ow = __shfl_xor_sync(0xffffffffu, vw, 4);
+    if (live) {
+      *reinterpret_cast<uint32_t*>(pg + P::k_code(b, row) + sub * 4) = kw;
+      if (pair) {
+        const bool odd = row & 1;
+        *reinterpret_cast<uint32_t*>(pg + P::v_piece(b, row & ~1, sub * 2 + (odd ? 1 : 0))) =
+            odd ? __byte_perm(ow, vw, 0x7632) : __byte_perm(vw, ow, 0x5410);
+      } else {
+        *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, row, sub * 2)) = (uint16_t)vw;
+        *reinterpret_cast<uint16_t*>(pg + P::v_piece(b, row, sub * 2 + 1)) = (uint16_t)(vw >> 16);
+      }
+    }
+  }
+  if (!live) return;
+  if (sub == 0) {
+    if constexpr (NB == 4)
+      *reinterpret_cast<uint2*>(pg + P::k_scale(0, row)) = make_uint2(ks[0] | ks[1] << 16, ks[2] | ks[3] << 16);
+    else
+      *reinterpret_cast<uint32_t*>(pg + P::k_scale(0, row)) = ks[0] | ks[1] << 16;
+    *reinterpret_cast<float*>(pg + P::logn(row)) = ln;
+  }
+  if (sub < NB) *reinterpret_cast<uint16_t*>(pg + P::v_scale(sub, row)) = (uint16_t)vs;
 }
 
 template <typename T, int D>
@@ -219,48 +240,68 @@ page_load_kernel(const unsigned char* __restrict__ pages, int n_slots,
                  const int32_t* __restrict__ slots, long long n_rows, T* __restrict__ K,
                  T* __restrict__ V, float* __restrict__ logn, int32_t* flags) {
   using P = PageLayout<D>;
-  constexpr int LPR = D / 8, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, c8 = lane % LPR, b = c8 / 4, sub = c8 % 4;
-  const long long nwarps = (long long)gridDim.x * (kRowThreads / 32);
-  for (long long r0 = ((long long)blockIdx.x * (kRowThreads / 32) + threadIdx.x / 32) * RPW;
-       r0 < n_rows; r0 += nwarps * RPW) {
-    const long long r = r0 + lane / LPR;
-    const int slot = r < n_rows ? slots[r] : -1;
-    if (slot < 0) continue;
-    if (slot >= n_slots) {
-      if (c8 == 0) set_flag(flags, KVS_FLAG_BAD_PAGE);
-      continue;
-    }
-    const unsigned char* pg = pages + (size_t)(slot / kPageRows) * P::kBytes;
-    const int row = slot % kPageRows;
-    const uint32_t kw = *reinterpret_cast<const uint32_t*>(pg + P::k_code(b, row) + sub * 4);
-    const uint32_t vw = *reinterpret_cast<const uint16_t*>(pg + P::v_piece(b, row, sub * 2)) |
-                        (uint32_t)*reinterpret_cast<const uint16_t*>(pg + P::v_piece(b, row, sub * 2 + 1)) << 16;
-    const float ks = __half2float(*reinterpret_cast<const __half*>(pg + P::k_scale(b, row)));
-    const float vs = __half2float(*reinterpret_cast<const __half*>(pg + P::v_scale(b, row)));
-    float x[8];
-    dequantise8(kw, ks, x);
-#pragma unroll
-    for (int i = 0; i < 8; i += Vec16<T>::n) store_vec(K + r * D + c8 * 8 + i, x + i);
-    dequantise8(vw, vs, x);
-#pragma unroll
-    for (int i = 0; i < 8; i += Vec16<T>::n) store_vec(V + r * D + c8 * 8 + i, x + i);
-    if (c8 == 0 && logn) logn[r] = *reinterpret_cast<const float*>(pg + P::logn(row));
+  constexpr int NB = P::nb;
+  const int lane = threadIdx.x & 31, sub = lane & 3;
+  const long long r = (long long)blockIdx.x * kRowsPerBlock + threadIdx.x / 4;
+  int slot = r < n_rows ? slots[r] : -1;
+  if (slot >= n_slots) {
+    if (sub == 0) set_flag(flags, KVS_FLAG_BAD_PAGE);
+    slot = -1;
   }
+  if (!__any_sync(0xffffffffu, slot >= 0)) return;
+  const bool live = slot >= 0, pair = paired(slot, lane);
+  const int row = slot & (kPageRows - 1);
+  const bool odd = row & 1;
+  const unsigned char* pg = pages + (size_t)(live ? slot / kPageRows : 0) * P::kBytes;
+  uint32_t kw[NB], vw[NB], vs = 0;
+  uint2 ks = make_uint2(0u, 0u);
+  float ln = 0.f;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) kw[b] = vw[b] = 0u;
+  if (live) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      kw[b] = __ldcs(reinterpret_cast<const uint32_t*>(pg + P::k_code(b, row) + sub * 4));
+      if (pair)
+        vw[b] = __ldcs(reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, row & ~1, sub * 2 + (odd ? 1 : 0))));
+      else
+        vw[b] = *reinterpret_cast<const uint16_t*>(pg + P::v_piece(b, row, sub * 2)) |
+                (uint32_t)*reinterpret_cast<const uint16_t*>(pg + P::v_piece(b, row, sub * 2 + 1)) << 16;
+    }
+    if constexpr (NB == 4)
+      ks = *reinterpret_cast<const uint2*>(pg + P::k_scale(0, row));
+    else
+      ks.x = *reinterpret_cast<const uint32_t*>(pg + P::k_scale(0, row));
+    if (sub < NB) vs = *reinterpret_cast<const uint16_t*>(pg + P::v_scale(sub, row));
+    if (sub == 0 && logn) ln = *reinterpret_cast<const float*>(pg + P::logn(row));
+  }
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const uint32_t ow = __shfl_xor_sync(0xffffffffu, vw[b], 4);
+    if (pair) vw[b] = odd ? __byte_perm(ow, vw[b], 0x7632) : __byte_perm(vw[b], ow, 0x5410);
+    const uint32_t sv = __shfl_sync(0xffffffffu, vs, (lane & ~3) + b);
+    const uint32_t sk = (b & 2 ? ks.y : ks.x) >> (b & 1 ? 16 : 0);
+    if (live) {
+      float x[8];
+      dequantise8(kw[b], __half2float(__ushort_as_half((unsigned short)sk)), x);
+#pragma unroll
+      for (int i = 0; i < 8; i += Vec16<T>::n) store_vec(K + r * D + b * 32 + sub * 8 + i, x + i);
+      dequantise8(vw[b], __half2float(__ushort_as_half((unsigned short)sv)), x);
+#pragma unroll
+      for (int i = 0; i < 8; i += Vec16<T>::n) store_vec(V + r * D + b * 32 + sub * 8 + i, x + i);
+    }
+  }
+  if (live && sub == 0 && logn) logn[r] = ln;
 }
 
-static int row_blocks(long long n_rows, int rows_per_warp) {
-  const long long per = (long long)(kRowThreads / 32) * rows_per_warp;
-  const long long n = (n_rows + per - 1) / per;
-  return (int)(n < (1ll << 20) ? n : (1ll << 20));
-}
+static int row_blocks(long long n_rows) { return (int)((n_rows + kRowsPerBlock - 1) / kRowsPerBlock); }
 
 template <typename T, int D>
 static cudaError_t store_t(const kvs_cache_desc& d, const void* K, const void* V,
                            const float* logn, const int32_t* slots, const kvs_page_pool& pool,
                            char* ws, cudaStream_t st) {
   const long long n = (long long)d.B * d.H_kv * d.T_cap;
-  page_store_kernel<T, D><<<row_blocks(n, 256 / D), kRowThreads, 0, st>>>(
+  page_store_kernel<T, D><<<row_blocks(n), kRowThreads, 0, st>>>(
       (const T*)K, (const T*)V, logn, slots, n, (unsigned char*)pool.pages,
       pool.n_pages * kPageRows, reinterpret_cast<int32_t*>(ws));
   count_launches(1);
@@ -271,7 +312,7 @@ template <typename T, int D>
 static cudaError_t load_t(const kvs_cache_desc& d, const kvs_page_pool& pool, const int32_t* slots,
                           void* K, void* V, float* logn, char* ws, cudaStream_t st) {
   const long long n = (long long)d.B * d.H_kv * d.T_cap;
-  page_load_kernel<T, D><<<row_blocks(n, 256 / D), kRowThreads, 0, st>>>(
+  page_load_kernel<T, D><<<row_blocks(n), kRowThreads, 0, st>>>(
       (const unsigned char*)pool.pages, pool.n_pages * kPageRows, slots, n, (T*)K, (T*)V, logn,
       reinterpret_cast<int32_t*>(ws));
   count_launches(1);

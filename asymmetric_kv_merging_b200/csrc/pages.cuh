@@ -67,7 +67,7 @@ __device__ __forceinline__ uint32_t scale_bits(float amax) {
 //
 // bf16 rows: x = m 2^e with m < 2^8, and a rounding border is (2k + 1) n 2^(f - 1) with
 // s = n 2^f, n < 2^11. Off a border, x is at least 2^(f - 1) or 2^e away from it, in units of s
-// at least 1 / 2n or 2^-8 x / s: more than 2^-12. x * (1/s) is off by at most 6.5 * 2^-24, so
+// at least 1 / 2n or 2^-8 x / s: more than 2^-12. x * (1/s) is off by at most 6.5 * 2^-23, so
 // adding 48 (last place 2^-18) puts a value on a border exactly back onto it and leaves the
 // others on their side; the second sum rounds to an integer, ties to even, and leaves c + 8 in
 // the low bits. fp32 rows: x and a border may be 2^-24 apart relative to each other, so the
@@ -75,42 +75,73 @@ __device__ __forceinline__ uint32_t scale_bits(float amax) {
 // border has 4 bits).
 template <typename T>
 __device__ __forceinline__ uint32_t quantise8(const float* x, uint32_t sb) {
-  uint32_t w = 0;
-  const float s = __half2float(__ushort_as_half((unsigned short)sb));
   if (sb == 0u || sb == 0x7fffu) return 0x88888888u;
+  const float s = __half2float(__ushort_as_half((unsigned short)sb));
+  uint32_t w = 0;
   if constexpr (sizeof(T) == 2) {
-    const float inv = __fdiv_rn(1.f, s);
+    float inv;                                         // off by a last place at most
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+    // the bits of the second sum are 0x4b400000 + code: all eight go into place by shift and add,
+    // and the eight constants come off in one piece (modulo 2^32)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float t = fmaf(x[i], inv, 48.f);
-      const uint32_t c = __float_as_uint(__fadd_rn(t, 12582912.f + 8.f - 48.f)) & 15u;
-      w |= c << (4 * i);
+      w += __float_as_uint(__fadd_rn(t, 12582912.f + 8.f - 48.f)) << (4 * i);
     }
+    w -= 0x4b400000u * 0x11111111u;
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int c = __float2int_rn(__fdiv_rn(x[i], s)) + 8;
-      w |= (uint32_t)c << (4 * i);
-    }
+    for (int i = 0; i < 8; ++i) w |= (uint32_t)(__float2int_rn(__fdiv_rn(x[i], s)) + 8) << (4 * i);
   }
   return w;
 }
 
+// 8 channels of a row as they are in the cache.
+template <typename T> struct Raw8;
+template <> struct Raw8<bf16> {
+  uint4 v;
+  __device__ __forceinline__ void load(const bf16* p) { v = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  // the largest magnitude; as integers, magnitudes order like their values, with infinities and
+  // NaN on top
+  __device__ __forceinline__ float amax() const {
+    const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+    return __uint_as_float(max(m << 16, m & 0xffff0000u));
+  }
+  __device__ __forceinline__ void widen(float* x) const {
+    x[0] = bf16_lo(v.x); x[1] = bf16_hi(v.x); x[2] = bf16_lo(v.y); x[3] = bf16_hi(v.y);
+    x[4] = bf16_lo(v.z); x[5] = bf16_hi(v.z); x[6] = bf16_lo(v.w); x[7] = bf16_hi(v.w);
+  }
+};
+template <> struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p));
+    b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float amax() const {
+    auto u = [](float f) { return __float_as_uint(f) & 0x7fffffffu; };
+    return __uint_as_float(max(max(max(u(a.x), u(a.y)), max(u(a.z), u(a.w))),
+                               max(max(u(b.x), u(b.y)), max(u(b.z), u(b.w)))));
+  }
+  __device__ __forceinline__ void widen(float* x) const {
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
+
 // Codes and scale of 8 channels of a row held by this lane, the 32 channels of a block being
 // held by four consecutive lanes (a multiple of 4 on). Whole warps take part.
 template <typename T>
-__device__ __forceinline__ uint32_t quantise_lane(const float* x, uint32_t& sb) {
-  float a = 0.f;
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a = fmaxf(a, fabsf(x[i]));
-    bad |= x[i] != x[i];                             // fmaxf drops a NaN
-  }
-  if (bad) a = INFINITY;
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 1));
-  a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, 2));
-  sb = scale_bits(a);
+__device__ __forceinline__ uint32_t quantise_lane(const Raw8<T>& raw, uint32_t& sb) {
+  uint32_t a = __float_as_uint(raw.amax());
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  sb = scale_bits(__uint_as_float(a));
+  float x[8];
+  raw.widen(x);
   return quantise8<T>(x, sb);
 }
 
