@@ -415,7 +415,7 @@ kvs_status kvs_page_assign(const kvs_page_pool* pool, int32_t units, const int32
     for (int j = i + 1; j < 5; ++j)
       if (overlap(outs[i], outs[j])) return KVS_ERR_ALIAS;
   }
-  s = check_ws(ws, ws_bytes, page_assign_bytes(units));
+  s = check_ws(ws, ws_bytes, page_assign_ws(units).total);
   if (s != KVS_OK) return s;
   return from_cuda(launch_page_assign(*pool, units, rows, held, free_pages, n_free, slot_begin,
                                       slots, slot_stride, static_cast<char*>(ws),

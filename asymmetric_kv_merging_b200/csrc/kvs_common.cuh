@@ -245,9 +245,18 @@ struct PageLayoutWs {
 inline size_t page_persistent_bytes(int units) {
   return kWsAlign + align_up((size_t)units * sizeof(int32_t), kWsAlign);
 }
-// scratch of the page table update: two offsets per unit, after the persistent region
-inline size_t page_assign_bytes(int units) {
-  return page_persistent_bytes(units) + align_up((size_t)units * 2 * sizeof(int32_t), kWsAlign);
+// Scratch of the page table update: two offsets per unit and their sums after the persistent
+// region; its CTAs count themselves in the flag word's block, as the decode's do.
+struct PageAssignWs {
+  size_t done, pre, sums, total;
+};
+inline PageAssignWs page_assign_ws(int units) {
+  PageAssignWs L;
+  L.done = kWsAlign * 3 / 4;
+  L.pre = page_persistent_bytes(units);
+  L.sums = align_up(L.pre + (size_t)units * 2 * sizeof(int32_t), 16);
+  L.total = align_up(L.sums + 16, kWsAlign);
+  return L;
 }
 
 inline PageLayoutWs page_layout_ws(const kvs_cache_desc& d) {
@@ -258,7 +267,7 @@ inline PageLayoutWs page_layout_ws(const kvs_cache_desc& d) {
   L.part = page_persistent_bytes(units);
   const size_t part = (size_t)kPageDecodeCtas * 2 * (d.H_q / d.H_kv) * (d.d + kPartPad) * sizeof(float);
   L.total = align_up(L.part + part, kWsAlign);
-  if (L.total < page_assign_bytes(units)) L.total = page_assign_bytes(units);
+  if (L.total < page_assign_ws(units).total) L.total = page_assign_ws(units).total;
   return L;
 }
 

@@ -16,39 +16,38 @@ namespace kvs {
 // Page tables from lengths
 // ---------------------------------------------------------------------------
 
-constexpr int kAssignThreads = 1024;
+constexpr int kAssignThreads = 512;
+constexpr int kAssignLocal = 4096;    // units whose offsets fit in shared memory (32 KB)
 
 struct UnitPages {
   int held, want;     // pages of the unit before and after (equal: nothing to do)
 };
 
+__device__ __forceinline__ bool unit_legal(int rows, int held, int max_pages) {
+  return held >= 0 && held <= max_pages && rows >= 0 && pages_of(rows) <= max_pages;
+}
 __device__ __forceinline__ UnitPages unit_pages(int rows, int held, int max_pages) {
   if (held < 0 || held > max_pages) return {0, 0};                       // left alone
   if (rows < 0 || pages_of(rows) > max_pages) return {held, held};
   return {held, pages_of(rows)};
 }
 
-// One CTA: exclusive sums of the pages each unit takes and gives back, then a warp per unit
-// moves the page numbers: first those given back onto the free stack, then those taken off it.
-__global__ void __launch_bounds__(kAssignThreads)
-page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* table,
-                   int32_t* free_pages, int32_t* n_free, int units, int n_pages, int max_pages,
-                   int2* __restrict__ offs, int32_t* flags) {
-  __shared__ longlong2 s_warp[kAssignThreads / 32];   // 64 bits: garbage lengths may add up to more
-  __shared__ longlong2 s_total;
+// Exclusive sums over the units of the pages they take (x) and give back (y) into pre[units];
+// the totals in 64 bits (garbage lengths may add up to more). One CTA.
+__device__ __forceinline__ longlong2 scan_units(const int32_t* rows, const int32_t* held, int units,
+                                                int max_pages, int2* pre, bool& bad) {
+  __shared__ longlong2 s_warp[kAssignThreads / 32 + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (units + kAssignThreads - 1) / kAssignThreads;
   const int u0 = min(units, tid * per), u1 = min(units, u0 + per);
   longlong2 sum = make_longlong2(0, 0);
-  bool bad = false;
   for (int u = u0; u < u1; ++u) {
     const int r = rows[u], h = held[u];
     const UnitPages p = unit_pages(r, h, max_pages);
-    bad |= h < 0 || h > max_pages || r < 0 || pages_of(r) > max_pages;
+    bad |= !unit_legal(r, h, max_pages);
     sum.x += max(0, p.want - p.held);
     sum.y += max(0, p.held - p.want);
   }
-  if (bad) set_flag(flags, KVS_FLAG_BAD_LENGTH);
   longlong2 inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -61,93 +60,183 @@ page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* tab
   }
   if (lane == 31) s_warp[warp] = inc;
   __syncthreads();
-  if (warp == 0) {
-    const longlong2 w = s_warp[lane];
-    longlong2 c = w;
+  longlong2 before = make_longlong2(0, 0), total = before;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, c.x, o);
-      const long long y = __shfl_up_sync(0xffffffffu, c.y, o);
-      if (lane >= o) {
-        c.x += x;
-        c.y += y;
-      }
-    }
-    if (lane == 31) s_total = c;
-    s_warp[lane] = make_longlong2(c.x - w.x, c.y - w.y);
+  for (int w = 0; w < kAssignThreads / 32; ++w) {
+    if (w == warp) before = total;
+    total.x += s_warp[w].x;
+    total.y += s_warp[w].y;
   }
-  __syncthreads();
-  const long long taken = s_total.x, given = s_total.y;
-  const int avail = *n_free;
-  const bool ok = avail >= 0 && avail + given <= n_pages && taken <= avail + given;
-  if (!ok) {
-    if (tid == 0) set_flag(flags, KVS_FLAG_NO_PAGES);
-    return;
-  }
-  int2 at = make_int2((int)(s_warp[warp].x + inc.x - sum.x), (int)(s_warp[warp].y + inc.y - sum.y));
+  int2 at = make_int2((int)(before.x + inc.x - sum.x), (int)(before.y + inc.y - sum.y));
   for (int u = u0; u < u1; ++u) {
-    offs[u] = at;
+    pre[u] = at;
     const UnitPages p = unit_pages(rows[u], held[u], max_pages);
     at.x += max(0, p.want - p.held);
     at.y += max(0, p.held - p.want);
   }
   __syncthreads();
-  for (int u = warp; u < units; u += kAssignThreads / 32) {
-    const UnitPages p = unit_pages(rows[u], held[u], max_pages);
-    const int o = avail + offs[u].y;
-    for (int j = p.want + lane; j < p.held; j += 32) {
-      int32_t* e = table + (size_t)u * max_pages + j;
-      free_pages[o + j - p.want] = *e;
-      *e = -1;
-    }
-  }
-  __syncthreads();
-  const int base = avail + (int)given - (int)taken;
-  for (int u = warp; u < units; u += kAssignThreads / 32) {
-    const int h = held[u];
-    const UnitPages p = unit_pages(rows[u], h, max_pages);
-    const int o = base + offs[u].x;
-    for (int j = p.held + lane; j < p.want; j += 32)
-      table[(size_t)u * max_pages + j] = free_pages[o + j - p.held];
-    __syncwarp();
-    if (lane == 0 && h >= 0 && h <= max_pages) held[u] = p.want;
-  }
-  __syncthreads();
-  if (tid == 0) *n_free = base;
+  return total;
 }
 
-// slots[u][i] = slot of row begin[u] + i, -1 past the unit's rows or where it holds no page.
-__global__ void __launch_bounds__(256)
-page_slots_kernel(const int32_t* __restrict__ rows, const int32_t* __restrict__ begin,
-                  const int32_t* __restrict__ held, const int32_t* __restrict__ table,
-                  int32_t* __restrict__ slots, int units, int max_pages, int stride) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= stride) return;
-  for (int u = blockIdx.y; u < units; u += gridDim.y) {
-    const int b = begin ? begin[u] : 0;
-    const long long t = (long long)b + i;
-    int slot = -1;
-    if (b >= 0 && t < rows[u] && t / kPageRows < min(held[u], max_pages)) {
-      const int pg = table[(size_t)u * max_pages + (int)(t / kPageRows)];
-      if (pg >= 0) slot = pg * kPageRows + (int)(t % kPageRows);
-    }
-    slots[(size_t)u * stride + i] = slot;
+// The unit that taken (or given) page i belongs to: the last one whose offset is not above i.
+template <bool kGiven>
+__device__ __forceinline__ int unit_of(const int2* pre, int units, int i) {
+  int lo = 0, hi = units - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if ((kGiven ? pre[mid].y : pre[mid].x) <= i) lo = mid;
+    else hi = mid - 1;
   }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kAssignThreads)
+page_scan_kernel(const int32_t* __restrict__ rows, const int32_t* __restrict__ held, int units,
+                 int max_pages, int2* pre, longlong2* total, int32_t* flags) {
+  bool bad = false;
+  const longlong2 t = scan_units(rows, held, units, max_pages, pre, bad);
+  if (bad) set_flag(flags, KVS_FLAG_BAD_LENGTH);
+  if (threadIdx.x == 0) *total = t;
+}
+
+// Moves the page numbers and writes the slot map, spread over the grid. The stack after the call
+// is the old one, with the given pages pushed and the taken ones popped; where a taken page is
+// one that is given in the same call, the thread that has it hands it on. So nothing of the
+// stack that is read is also written, and no CTA waits for another; what other CTAs still read
+// (the held counts, and the table entries of given pages if a slot map has to find those) is
+// written by the last CTA to finish.
+// Small: latency-bound (a launch, the lengths, a page number, its slot). Large: the slot map's
+// writes. Sums and searches per CTA cost less than a second launch would.
+template <bool kLocal>
+__global__ void __launch_bounds__(kAssignThreads)
+page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* table,
+                   int32_t* free_pages, int32_t* n_free, const int32_t* __restrict__ begin,
+                   int32_t* __restrict__ slots, int stride, int units, int n_pages, int max_pages,
+                   int2* ws_pre, const longlong2* ws_total, int32_t* done, int32_t* flags) {
+  __shared__ int2 s_pre[kLocal ? kAssignLocal : 1];
+  __shared__ int s_last;
+  const int tid = threadIdx.x;
+  const int avail = *n_free;
+  int2* pre = kLocal ? s_pre : ws_pre;
+  longlong2 total;
+  if constexpr (kLocal) {
+    bool bad = false;
+    total = scan_units(rows, held, units, max_pages, s_pre, bad);
+    if (bad && blockIdx.x == 0) set_flag(flags, KVS_FLAG_BAD_LENGTH);
+  } else {
+    total = *ws_total;
+  }
+  const bool ok = avail >= 0 && avail + total.y <= n_pages && total.x <= avail + total.y;
+  const int taken = ok ? (int)total.x : 0, given = ok ? (int)total.y : 0;
+  const int top = avail + given - taken;               // the stack's size afterwards
+  const bool keep = slots != nullptr && taken > 0;     // given entries stay until the end
+  const long long gtid = (long long)blockIdx.x * kAssignThreads + tid;
+  const long long gsize = (long long)gridDim.x * kAssignThreads;
+  auto entry = [&](int u, int j) -> int32_t& { return table[(size_t)u * max_pages + j]; };
+  auto given_at = [&](int i) -> int32_t& {
+    const int u = unit_of<true>(pre, units, i);
+    return entry(u, unit_pages(rows[u], held[u], max_pages).want + i - pre[u].y);
+  };
+  auto taken_at = [&](int i) -> int32_t& {
+    const int u = unit_of<false>(pre, units, i);
+    return entry(u, held[u] + i - pre[u].x);
+  };
+  for (long long i = gtid; i < given; i += gsize) {
+    int32_t& e = given_at((int)i);
+    const int at = avail + (int)i;                     // its place on the stack
+    if (at < top) free_pages[at] = e;
+    else taken_at(at - top) = e;
+    if (!keep) e = -1;
+  }
+  for (long long i = gtid; i < taken - given; i += gsize) taken_at((int)i) = free_pages[top + i];
+
+  if (slots != nullptr) {
+    // four slots a thread, of at most two pages
+    const int quads = (stride + 3) / 4;
+    for (long long q = gtid; q < (long long)units * quads; q += gsize) {
+      const int u = (int)(q / quads), i0 = (int)(q % quads) * 4;
+      const int b = begin ? begin[u] : 0, r = rows[u], h = held[u];
+      const UnitPages p = ok ? unit_pages(r, h, max_pages) : UnitPages{h, h};
+      const int np = min(p.want, max_pages);           // pages that the unit has afterwards
+      auto page = [&](int j) -> int {
+        if (j >= np) return -1;
+        if (j < p.held) return entry(u, j);
+        const int at = top + pre[u].x + j - p.held;
+        return at < avail ? free_pages[at] : given_at(at - avail);
+      };
+      int out[4], j_of = -1, id = -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const long long t = (long long)b + i0 + k;
+        out[k] = -1;
+        if (b >= 0 && t < r) {
+          const int j = (int)(t / kPageRows);
+          if (j != j_of) {
+            j_of = j;
+            id = page(j);
+          }
+          if (id >= 0) out[k] = id * kPageRows + (int)(t % kPageRows);
+        }
+      }
+      int32_t* o = slots + (size_t)u * stride + i0;
+      if (stride % 4 == 0 && (reinterpret_cast<uintptr_t>(slots) & 15) == 0) {
+        *reinterpret_cast<int4*>(o) = make_int4(out[0], out[1], out[2], out[3]);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (i0 + k < stride) o[k] = out[k];
+      }
+    }
+  }
+  if (!ok) {
+    if (gtid == 0) set_flag(flags, KVS_FLAG_NO_PAGES);
+    return;                                            // (in every CTA)
+  }
+  __syncthreads();
+  if (gridDim.x > 1) {
+    if (tid == 0) s_last = atom_add_acq_rel_gpu(done, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    if (tid == 0) *done = 0;
+  }
+  if (keep) {
+    for (int i = tid; i < given; i += kAssignThreads) {
+      // (a handed-on page's new entry is never one of these: those units only give)
+      given_at(i) = -1;
+    }
+    __syncthreads();
+  }
+  for (int u = tid; u < units; u += kAssignThreads) {
+    const int h = held[u];
+    if (h >= 0 && h <= max_pages) held[u] = unit_pages(rows[u], h, max_pages).want;
+  }
+  if (tid == 0) *n_free = top;
 }
 
 cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32_t* rows,
                                int32_t* held, int32_t* free_pages, int32_t* n_free,
                                const int32_t* begin, int32_t* slots, int stride, char* ws,
                                cudaStream_t st) {
-  page_assign_kernel<<<1, kAssignThreads, 0, st>>>(
-      rows, held, pool.table, free_pages, n_free, units, pool.n_pages, pool.max_pages,
-      reinterpret_cast<int2*>(ws + page_persistent_bytes(units)), reinterpret_cast<int32_t*>(ws));
-  count_launches(1);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || !slots) return e;
-  const dim3 grid((stride + 255) / 256, units < 65535 ? units : 65535);
-  page_slots_kernel<<<grid, 256, 0, st>>>(rows, begin, held, pool.table, slots, units,
-                                          pool.max_pages, stride);
+  const PageAssignWs Ly = page_assign_ws(units);
+  int2* pre = reinterpret_cast<int2*>(ws + Ly.pre);
+  longlong2* total = reinterpret_cast<longlong2*>(ws + Ly.sums);
+  int32_t* flags = reinterpret_cast<int32_t*>(ws);
+  // one CTA for what a CTA does in a few steps, else enough for four slots (or eight page
+  // numbers, if every page moved) a thread, up to one CTA per SM
+  const long long work = (long long)units * stride / 4 > (long long)units * pool.max_pages / 8
+                             ? (long long)units * stride / 4 : (long long)units * pool.max_pages / 8;
+  long long ctas = (work + kAssignThreads - 1) / kAssignThreads;
+  if (ctas > kTargetCtas / 2) ctas = kTargetCtas / 2;
+  if (ctas < 1) ctas = 1;
+  const bool local = units <= kAssignLocal;
+  if (!local) {
+    page_scan_kernel<<<1, kAssignThreads, 0, st>>>(rows, held, units, pool.max_pages, pre, total, flags);
+    count_launches(1);
+  }
+  auto kfn = local ? page_assign_kernel<true> : page_assign_kernel<false>;
+  kfn<<<(int)ctas, kAssignThreads, 0, st>>>(rows, held, pool.table, free_pages, n_free, begin, slots,
+                                            stride, units, pool.n_pages, pool.max_pages, pre, total,
+                                            reinterpret_cast<int32_t*>(ws + Ly.done), flags);
   count_launches(1);
   return cudaGetLastError();
 }
