@@ -139,6 +139,7 @@ def _ptr(t: Optional[torch.Tensor]):
 
 # the handle of a device's current stream without building a Stream object (3 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch.cuda.current_device
 
 
 def _stream(stream) -> int:
@@ -284,21 +285,24 @@ def page_pool(pages: torch.Tensor, table: torch.Tensor) -> PagePool:
     return pool
 
 
-def _arg(t: Optional[torch.Tensor], dtype, n: int, device: int):
+_I32, _U8, _FP32 = torch.int32, torch.uint8, torch.float32
+
+
+def _arg(t, dtype, n, device):
     """Raw pointer of a tensor that the library reads or writes as n elements of dtype; a wrong
     type, size, device or layout would be read as something else, so it raises."""
     if t is None:
         return None
-    if t.dtype is not dtype or t.numel() != n or t.get_device() != device or not t.is_contiguous():
-        raise ValueError(f"expected a contiguous {dtype} tensor of {n} elements on cuda:{device}, "
-                         f"not {t.dtype} of {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.numel() == n and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"expected a contiguous {dtype} tensor of {n} elements on cuda:{device}, "
+                     f"not {t.dtype} of {tuple(t.shape)} on {t.device}")
 
 
 def _pool_device(pool: PagePool, units: int, d: Optional[int] = None) -> int:
     """The device of a call on `pool`, which has to be the current one (kernels launch there)."""
     device = pool.device
-    if device != torch.cuda.current_device():
+    if device != _current_device():
         raise ValueError(f"the pool is on {pool.tensors[0].device}, which is not the current device")
     if pool.units < units:
         raise ValueError(f"the pool has tables of {pool.units} units, not {units}")
@@ -307,23 +311,20 @@ def _pool_device(pool: PagePool, units: int, d: Optional[int] = None) -> int:
     return device
 
 
-def _page_stream(stream, device: int) -> int:
-    return _raw_stream(device) if stream is None else stream.cuda_stream
-
-
 def page_assign(pool, rows, held, free_pages, n_free, ws, slots=None, slot_begin=None, stream=None):
     """kvs_page_assign: every unit of rows [units] holds the pages of its rows; with slots
     [units, stride], the slots of its rows from slot_begin on."""
     units = rows.numel()
     dev = _pool_device(pool, units)
     stride = 0 if slots is None else slots.shape[-1]
-    i32 = torch.int32
-    _check(_lib.kvs_page_assign(
-        pool, units, _arg(rows, i32, units, dev), _arg(held, i32, units, dev),
-        _arg(free_pages, i32, pool.n_pages, dev), _arg(n_free, i32, 1, dev),
-        _arg(slot_begin, i32, units, dev), _arg(slots, i32, units * stride, dev), stride,
-        _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(), _page_stream(stream, dev)),
-        "kvs_page_assign")
+    nws = ws.numel()
+    st = _lib.kvs_page_assign(
+        pool, units, _arg(rows, _I32, units, dev), _arg(held, _I32, units, dev),
+        _arg(free_pages, _I32, pool.n_pages, dev), _arg(n_free, _I32, 1, dev),
+        _arg(slot_begin, _I32, units, dev), _arg(slots, _I32, units * stride, dev), stride,
+        _arg(ws, _U8, nws, dev), nws, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise KvsError(st, "kvs_page_assign")
 
 
 def page_store(desc, K, V, logn, slots, pool, ws, stream=None):
@@ -331,11 +332,13 @@ def page_store(desc, K, V, logn, slots, pool, ws, stream=None):
     d, dtype = desc.d, _DTYPES[desc.dtype]
     rows = desc.B * desc.H_kv * desc.T_cap
     dev = _pool_device(pool, 0, d)
-    _check(_lib.kvs_page_store(
+    nws = ws.numel()
+    st = _lib.kvs_page_store(
         desc, _arg(K, dtype, rows * d, dev), _arg(V, dtype, rows * d, dev),
-        _arg(logn, torch.float32, rows, dev), _arg(slots, torch.int32, rows, dev), pool,
-        _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(), _page_stream(stream, dev)),
-        "kvs_page_store")
+        _arg(logn, _FP32, rows, dev), _arg(slots, _I32, rows, dev), pool, _arg(ws, _U8, nws, dev), nws,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise KvsError(st, "kvs_page_store")
 
 
 def page_load(desc, pool, slots, K, V, logn, ws, stream=None):
@@ -343,20 +346,23 @@ def page_load(desc, pool, slots, K, V, logn, ws, stream=None):
     d, dtype = desc.d, _DTYPES[desc.dtype]
     rows = desc.B * desc.H_kv * desc.T_cap
     dev = _pool_device(pool, 0, d)
-    _check(_lib.kvs_page_load(
-        desc, pool, _arg(slots, torch.int32, rows, dev), _arg(K, dtype, rows * d, dev),
-        _arg(V, dtype, rows * d, dev), _arg(logn, torch.float32, rows, dev),
-        _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(), _page_stream(stream, dev)),
-        "kvs_page_load")
+    nws = ws.numel()
+    st = _lib.kvs_page_load(
+        desc, pool, _arg(slots, _I32, rows, dev), _arg(K, dtype, rows * d, dev),
+        _arg(V, dtype, rows * d, dev), _arg(logn, _FP32, rows, dev), _arg(ws, _U8, nws, dev), nws,
+        _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise KvsError(st, "kvs_page_load")
 
 
 def page_decode_attn(desc, q, pool, lens, out, ws, k_new=None, v_new=None, stream=None):
     """kvs_page_decode_attn: one decode step over the pages of every unit."""
     d, dtype, units = desc.d, _DTYPES[desc.dtype], desc.B * desc.H_kv
     dev = _pool_device(pool, units, d)
-    n = desc.B * desc.H_q * d
-    _check(_lib.kvs_page_decode_attn(
-        desc, _arg(q, dtype, n, dev), pool, _arg(lens, torch.int32, units, dev),
-        _arg(k_new, dtype, units * d, dev), _arg(v_new, dtype, units * d, dev),
-        _arg(out, dtype, n, dev), _arg(ws, torch.uint8, ws.numel(), dev), ws.numel(),
-        _page_stream(stream, dev)), "kvs_page_decode_attn")
+    n, nws = desc.B * desc.H_q * d, ws.numel()
+    st = _lib.kvs_page_decode_attn(
+        desc, _arg(q, dtype, n, dev), pool, _arg(lens, _I32, units, dev),
+        _arg(k_new, dtype, units * d, dev), _arg(v_new, dtype, units * d, dev), _arg(out, dtype, n, dev),
+        _arg(ws, _U8, nws, dev), nws, _raw_stream(dev) if stream is None else stream.cuda_stream)
+    if st:
+        raise KvsError(st, "kvs_page_decode_attn")
