@@ -28,6 +28,7 @@ namespace kvs {
 constexpr int kPdWarps = 8;
 constexpr int kPdThreads = kPdWarps * 32;
 constexpr int kPdStages = 2;
+constexpr int kPdLens = kPdThreads;    // units of a CTA whose lengths it keeps in shared memory
 
 template <int D, int G>
 struct PageDecodeShape {
@@ -66,7 +67,7 @@ static bool use_cluster(int C, int max_pages) { return C >= 8 && max_pages <= 12
 
 // Places of a unit in the numbering: its pages, and some for the work at its end (an empty unit
 // has a place, so that a CTA finishes it).
-constexpr int kUnitPages = 8;
+constexpr int kUnitPages = 12;
 __device__ __forceinline__ int unit_span(int L) { return pages_of(L) + kUnitPages; }
 
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
@@ -698,11 +699,11 @@ page_decode_kernel(const PageArgs<T> a) {
   __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
   __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
   __shared__ float s_m[NW][G], s_l[NW][G], s_stat[G][2];
-  // the new row's logits and page for the unit that began in an earlier CTA (0), the one that
-  // goes on in a later one (1), and units that are whole here (2 and 3 in turn)
-  __shared__ float s_new[4][G];
-  __shared__ int s_page[4];
-  __shared__ int4 s_split[2];     // units 0 and 1: unit, first CTA, CTAs, length
+  __shared__ float s_new[3][G];   // the new row's logits, for the units of s_split and a whole one
+  __shared__ int s_len[kPdLens];  // lengths (as they are in memory) of units from the first one on
+  // the unit that began in an earlier CTA (0) and the one that goes on in a later one (1): unit,
+  // first CTA, CTAs, length
+  __shared__ int4 s_split[2];
   __shared__ int s_last[2];
 
   griddep_wait();                 // launched with programmatic stream serialisation
@@ -725,22 +726,49 @@ page_decode_kernel(const PageArgs<T> a) {
   const int chunk = max(NW, (total + (int)gridDim.x - 1) / (int)gridDim.x);
   const int f0 = (int)min((long long)total, (long long)blockIdx.x * chunk);
   const int f1 = (int)min((long long)total, (long long)f0 + chunk);
+  // Lengths move on when every CTA has read them, so this CTA says when it has: once the ones
+  // of its own units are in shared memory, while the first pages are on their way. (A CTA with
+  // more units than fit there reads on from memory, and says so at its end.)
+  bool told = false;
+  auto tell = [&]() {                                  // one warp
+    int last = 0;
+    if (lane == 0) last = atom_add_acq_rel_gpu(a.done, 1) == (int)gridDim.x - 1;
+    if (!__shfl_sync(0xffffffffu, last, 0)) return;
+    for (int u = lane; u < a.units; u += 32) {
+      const int L = a.len[u];
+      if (a.new_page(u, L) >= 0) a.len[u] = L + 1;
+    }
+    if (lane == 0) *a.done = 0;
+  };
 
   if (f0 < f1) {
     struct Place {
       int u, L;
       int at, end;                 // the unit's pages are [at, end)
     };
-    auto append = [&](int u, int L, int id) {
+    // The new row of a unit that is being finished: its page (-1: none) with its logits in s_new
+    // after the next barrier, and its place in the cache.
+    // (`len`: the unit's length as it is in memory, which may be out of range)
+    auto new_row = [&](int u, int len, int slot) {
+      const int id = a.k_new != nullptr ? a.new_page(u, len) : -1;
+      if (id >= 0 && warp < G) {
+        const float sn = new_logit<T, D, G>(a, u, warp, lane);
+        if (lane == 0) s_new[slot][warp] = sn;
+      }
+      return id;
+    };
+    auto append = [&](int u, int len, int id) {
       if (id >= 0)
-        write_new_row<T, D>(a, u, L, id, warp, lane);
-      else if (tid == 0 && a.len[u] == L)
+        write_new_row<T, D>(a, u, len, id, warp, lane);
+      else if (a.k_new != nullptr && tid == 0 && a.legal(len) == len)
         set_flag(a.flags, KVS_FLAG_OUT_CAPACITY);
     };
+    int u_first = 0;
+    auto len_of = [&](int u) { return told ? s_len[u - u_first] : a.len[u]; };
     auto move_to = [&](Place& p, int f) {
       while (f >= p.end) {
         ++p.u;
-        p.L = a.legal(a.len[p.u]);
+        p.L = a.legal(len_of(p.u));
         p.at = p.end;
         p.end = p.at + unit_span(p.L);
       }
@@ -793,28 +821,31 @@ page_decode_kernel(const PageArgs<T> a) {
     PageRing<D, ST> pr;
     pr.start(a.pages, dsm + warp * ST * P::kBytes,
              reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc) + warp * ST, fill(), lane);
+    if (a.k_new != nullptr) {
+      u_first = cp.u;
+      const int n = (f1 - cp.at) / kUnitPages + 1;     // no more units than that begin before f1
+      if (n <= kPdLens) {
+        if (tid < n && cp.u + tid < a.units) s_len[tid] = a.len[cp.u + tid];
+        __syncthreads();
+        told = true;
+        if (warp == NW - 1) tell();
+      }
+    }
 
-    int whole = 2;
     for (int seg = f0; seg < f1;) {
       move_to(cp, seg);
-      const int u = cp.u, L = cp.L;
+      const int u = cp.u;
       const int seg_end = min(f1, cp.end);
       const int first = cp.at / chunk, nsplit = (cp.end - 1) / chunk - first + 1;
-      const int slot = nsplit == 1 ? whole : (int)blockIdx.x == first ? 1 : 0;
+      const int slot = (int)blockIdx.x == first ? 1 : 0;
       if constexpr (sizeof(T) == 4) {
         for (int i = tid; i < G * D; i += kPdThreads)
           (&qs[0][0])[i] = to_f32(a.q[(size_t)u * G * D + i]) * (kLog2e / sqrtf((float)D));
         __syncthreads();
       }
       pw.begin(reinterpret_cast<const float(*)[D]>(qs), lane);
-      if (a.k_new != nullptr) {    // while the pages are on their way
-        const int id = a.new_page(u, a.len[u]);
-        if (id >= 0 && warp < G) {
-          const float sn = new_logit<T, D, G>(a, u, warp, lane);
-          if (lane == 0) s_new[slot][warp] = sn;
-        }
-        if (tid == 0) s_page[slot] = id;
-      }
+      if (a.k_new != nullptr && nsplit == 1 && tid < 2)    // wanted at the unit's end
+        prefetch_l2((tid == 0 ? a.k_new : a.v_new) + (size_t)u * D);
       static_assert(G <= NW, "a warp per query head");
       if (!pr.run((seg_end - f0 - warp + NW - 1) / NW, lane, fill,
                   [&](unsigned char* pg, int n) { pw.take(pg, n, lane); })) {
@@ -823,6 +854,8 @@ page_decode_kernel(const PageArgs<T> a) {
       }
       if (seg_end < f1) pw.load(a.q + (size_t)(u + 1) * G * D, lane);
       if (seg != f0) __syncthreads();              // the last unit's partials have been read
+      const int len = len_of(u);
+      const int id = nsplit == 1 ? new_row(u, len, 2) : -1;
       pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
       __syncthreads();
       if (tid < G * D / 4) {
@@ -830,8 +863,7 @@ page_decode_kernel(const PageArgs<T> a) {
         float M, Ls;
         const float4 A = merge_warps<D, G, NW>(s_acc, s_m, s_l, g, c, M, Ls);
         if (nsplit == 1) {
-          const bool fits = a.k_new != nullptr && s_page[slot] >= 0;
-          finish_columns<T>(A, M, Ls, fits ? s_new[slot][g] : -INFINITY, a.v_new + (size_t)u * D + c,
+          finish_columns<T>(A, M, Ls, id >= 0 ? s_new[2][g] : -INFINITY, a.v_new + (size_t)u * D + c,
                             a.out + (size_t)u * G * D + tid * 4);
         } else {
           // a row of the workspace; who finishes the unit is settled after this CTA's last page
@@ -840,12 +872,10 @@ page_decode_kernel(const PageArgs<T> a) {
           if (c == 0) *reinterpret_cast<float2*>(row + D) = make_float2(M, Ls);
         }
       }
-      if (nsplit == 1) {
-        if (a.k_new != nullptr) append(u, L, s_page[slot]);
-        whole ^= 1;
-      } else if (tid == 0) {
-        s_split[slot] = make_int4(u, first, nsplit, L);
-      }
+      if (nsplit == 1)
+        append(u, len, id);
+      else if (tid == 0)
+        s_split[slot] = make_int4(u, first, nsplit, len);
       seg = seg_end;
     }
 
@@ -855,6 +885,12 @@ page_decode_kernel(const PageArgs<T> a) {
     if (tid < 2) {
       const int4 sp = s_split[tid];
       s_last[tid] = sp.x >= 0 && atom_add_acq_rel_gpu(&a.counters[sp.x], 1) == sp.z - 1;
+    }
+    int new_id[2];                                 // (loads that overlap the arrivals')
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int4 sp = s_split[i];
+      new_id[i] = sp.x >= 0 ? new_row(sp.x, sp.w, i) : -1;
     }
     __syncthreads();
 #pragma unroll 1
@@ -878,6 +914,7 @@ page_decode_kernel(const PageArgs<T> a) {
             v[j] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + j * NGRP) + g * RS + c));
       };
       load_batch(grp);                             // with the factors' loads: one round trip for both
+      const int id = i == 0 ? new_id[0] : new_id[1];
       if (warp < G) {
         constexpr int kPer = (kPageDecodeCtas + 31) / 32;
         float2 ml[kPer];
@@ -928,27 +965,17 @@ page_decode_kernel(const PageArgs<T> a) {
           }
       }
       if (grp == 0) {
-        const bool fits = a.k_new != nullptr && s_page[i] >= 0;
-        finish_columns<T>(A, s_stat[g][0], s_stat[g][1], fits ? s_new[i][g] : -INFINITY,
+        finish_columns<T>(A, s_stat[g][0], s_stat[g][1], id >= 0 ? s_new[i][g] : -INFINITY,
                           a.v_new + (size_t)u * D + c, a.out + (size_t)u * G * D + unit * 4);
       }
-      if (a.k_new != nullptr) append(u, sp.w, s_page[i]);
+      append(u, sp.w, id);
       if (tid == 0) a.counters[u] = 0;
       __syncthreads();            // the shared arrays are free for the other unit
     }
   }
-  if (a.k_new != nullptr) {
-    // every CTA reads every length: they move on once the last CTA is through
+  if (a.k_new != nullptr && !told) {
     __syncthreads();
-    if (tid == 0) s_last[0] = atom_add_acq_rel_gpu(a.done, 1) == (int)gridDim.x - 1;
-    __syncthreads();
-    if (s_last[0]) {
-      for (int u = tid; u < a.units; u += kPdThreads) {
-        const int L = a.len[u];
-        if (a.new_page(u, L) >= 0) a.len[u] = L + 1;
-      }
-      if (tid == 0) *a.done = 0;
-    }
+    if (warp == 0) tell();
   }
 }
 
@@ -1070,6 +1097,12 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   cluster_wait();                 // no CTA leaves while a peer may read its shared memory
 }
 
+// Raises a kernel's dynamic shared-memory limit. The default one counts its static arrays too, so
+// it is raised whenever the sum could pass it.
+static bool allow_smem(const void* fn, size_t bytes) {
+  return ensure_smem_attr(fn, bytes > 48 * 1024 ? bytes : 48 * 1024 + 16);
+}
+
 // Cluster size for a cluster per unit on the current device, or 0 when the split kernel is to be
 // used: the largest C <= 16 with C * units <= SM count for which the occupancy calculator places
 // all clusters at once. Cached per device and number of units.
@@ -1089,7 +1122,7 @@ static int page_cluster_size(int units) {
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int C = sms / units;
   if (C > kMaxClusterSize) C = kMaxClusterSize;
-  if (!ensure_smem_attr((const void*)kfn, S::kSmem)) C = 0;
+  if (!allow_smem((const void*)kfn, S::kSmem)) C = 0;
   if (C > 8 && !ensure_nonportable_cluster((const void*)kfn)) C = 8;
   for (; C >= 2; --C) {
     cudaLaunchConfig_t cfg = {};
@@ -1145,7 +1178,7 @@ static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_pa
   }
   auto kfn = page_decode_kernel<T, D, G>;
   using S = PageDecodeShape<D, G>;
-  if (!ensure_smem_attr((const void*)kfn, S::kSmem)) return cudaErrorInvalidValue;
+  if (!allow_smem((const void*)kfn, S::kSmem)) return cudaErrorInvalidValue;
   const cudaError_t e = launch_pdl(kfn, dim3(kPageDecodeCtas), dim3(kPdThreads), S::kSmem, st, a);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
