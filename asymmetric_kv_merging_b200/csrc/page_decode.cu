@@ -209,13 +209,16 @@ struct PageWarp<bf16, D, G> {
   float lim0, lim1;            // a logit over the reference by more than this moves it
   float O[NB][2][4];           // sums of u w, of channels 4 g (+ 2) and of 4 g + 1 (+ 3) times 16 plus it
   float off[4];                // row b: sum_t p scale of block b; row 4: sum_t p
-  uint32_t ones;               // shared memory: 16 bytes of 1.0, 16 bytes of 0
+  // where this lane's row of `za` in take() is: 1 and an offset in the page, or 0 and an address
+  uint32_t za_page, za_off;
   uint32_t poison;             // bit b: block b of some row reads as NaN
 
   // `ones_`: 32 bytes of shared memory of this warp's own
   __device__ __forceinline__ void init(__half* ones_, int lane) {
     if (lane < 16) ones_[lane] = __float2half_rn(lane < 8 ? 1.f : 0.f);
-    ones = smem_u32(ones_);
+    const int row = lane & 7;
+    za_page = row < NB ? 1u : 0u;
+    za_off = row < NB ? P::kVs + row * 64 + (lane >> 3) * 16 : smem_u32(ones_) + (row == 4 ? 0u : 16u);
   }
 
   __device__ __forceinline__ void load(const bf16* q, int lane) {
@@ -323,9 +326,7 @@ struct PageWarp<bf16, D, G> {
       }
       const uint32_t za = as_u32(t & 1 ? sa[i][NB / 2 - 1] : sa[i][0]);
       const uint32_t zb = as_u32(t & 1 ? sb[i][NB / 2 - 1] : sb[i][0]);
-      x[i][0] = x[i][2] = r0;
-      x[i][1] = x[i][3] = r1;
-      mma_f16_16816(x[i], za, zb, za, zb, cb[0], cb[1]);
+      mma_f16_16816_from(x[i], za, zb, za, zb, cb[0], cb[1], r0, r1);
     }
     const uint32_t base = smem_u32(pg);
 #pragma unroll
@@ -399,11 +400,7 @@ struct PageWarp<bf16, D, G> {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
       ldsm_x4(base + P::v_scale(b, 0) + (lane >> 3) * 16, sv[b][0], sv[b][1], sv[b][2], sv[b][3]);
-    {
-      const int row = lane & 7;
-      ldsm_x4(row < NB ? base + P::kVs + row * 64 + (lane >> 3) * 16 : ones + (row == 4 ? 0u : 16u),
-              za[0], za[1], za[2], za[3]);
-    }
+    ldsm_x4(base * za_page + za_off, za[0], za[1], za[2], za[3]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i * 16 + 2 * t;
@@ -514,8 +511,8 @@ struct PageRing {
   uint64_t* full;
   uint32_t list, next;           // the list that page k + ST is on, and the one after it
   uint32_t due[ST];              // entries of the pages from k on
-  int k, stage;
-  uint32_t phase;                // bit s: parity of stage s
+  uint32_t parity[ST];           // of their stages
+  int k, stage, ahead;           // the next page, its stage, the place of page k + ST - 1 in its list
 
   __device__ __forceinline__ void issue(int s, uint32_t e, int lane) {
     if (e != 0u && lane == 0) {
@@ -523,7 +520,7 @@ struct PageRing {
       bulk_load(ring + s * P::kBytes, pages + (size_t)(e >> 6) * P::kBytes, P::kBytes, &full[s]);
     }
   }
-  // `first` is list 0. The copies of the first ST pages go out.
+  // `first` is list 0. The copies of the first ST pages go out; then the caller sets `next`.
   __device__ __forceinline__ void start(unsigned char* pages_, unsigned char* ring_, uint64_t* full_,
                                         uint32_t first, int lane) {
     pages = pages_;
@@ -531,7 +528,7 @@ struct PageRing {
     full = full_;
     list = first;
     k = stage = 0;
-    phase = 0u;
+    ahead = ST - 1;
     if (lane == 0) {
       for (int s = 0; s < ST; ++s) mbar_init(&full[s], 1);
       fence_mbar_init();
@@ -540,6 +537,7 @@ struct PageRing {
 #pragma unroll
     for (int s = 0; s < ST; ++s) {
       due[s] = __shfl_sync(0xffffffffu, list, s);
+      parity[s] = 0u;
       issue(s, due[s], lane);
     }
   }
@@ -551,28 +549,31 @@ struct PageRing {
     for (; k < kend; ++k) {
       const uint32_t cur = due[0];
       if (cur != 0u) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase >> stage & 1u))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(full + stage, parity[0]))) {
 #pragma unroll
           for (int i = 0; i < ST; ++i) {
-            const int s = (stage + i) % ST;
-            if (due[i] != 0u) mbar_wait(&full[s], phase >> s & 1u);
+            if (due[i] != 0u) mbar_wait(full + (stage + i) % ST, parity[i]);
             due[i] = 0u;
           }
           list = next = 0u;
           return false;
         }
-        phase ^= 1u << stage;
+        parity[0] ^= 1u;
         take(ring + stage * P::kBytes, (int)(cur & 63u));
         __syncwarp();
       }
-      const int ahead = (k + ST) & 31;
-      if (k == 0) next = fill();
+      ahead = (ahead + 1) & 31;
       if (ahead == 0) {
         list = next;
         next = fill();
       }
+      const uint32_t par = parity[0];
 #pragma unroll
-      for (int i = 0; i + 1 < ST; ++i) due[i] = due[i + 1];
+      for (int i = 0; i + 1 < ST; ++i) {
+        due[i] = due[i + 1];
+        parity[i] = parity[i + 1];
+      }
+      parity[ST - 1] = par;
       due[ST - 1] = __shfl_sync(0xffffffffu, list, ahead);
       issue(stage, due[ST - 1], lane);
       stage = stage + 1 == ST ? 0 : stage + 1;
@@ -831,6 +832,7 @@ page_decode_kernel(const PageArgs<T> a) {
         if (warp == NW - 1) tell();
       }
     }
+    pr.next = fill();
 
     for (int seg = f0; seg < f1;) {
       move_to(cp, seg);
@@ -1024,6 +1026,7 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   PageRing<D, ST> pr;
   pr.start(a.pages, dsm + warp * ST * P::kBytes,
            reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc + S::kSum) + warp * ST, entry(), lane);
+  pr.next = fill();
   if constexpr (sizeof(T) == 4) {
     for (int i = tid; i < G * D; i += NW * 32)
       (&qs[0][0])[i] = to_f32(a.q[(size_t)u * G * D + i]) * (kLog2e / sqrtf((float)D));
