@@ -73,8 +73,9 @@ __device__ __forceinline__ int unit_span(int L) { return pages_of(L) + kUnitPage
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// One warp's share of a unit: its softmax state over the pages it has taken. load() and begin()
-// take the unit's queries, take() adds the first nval rows of a page, end() writes the partial output
+// One warp's share of a unit: its softmax state over the pages it has taken. load() and prepare()
+// make the unit's operands from its queries (share() and fetch() hand them from one warp to the
+// others), reset() starts a unit, take() adds the first nval rows of a page, end() writes the partial output
 // [G][D] and (m, l) per query head (log2 domain; m is a reference, not always the maximum).
 
 // fp32: CUDA cores, every product and sum in fp32. Logits with a lane per row, values with a lane
@@ -84,13 +85,19 @@ template <typename T, int D, int G>
 struct PageWarp {
   using P = PageLayout<D>;
   static constexpr int QL = D / 4, RPS = 32 / QL;       // lanes per row of V, rows at a time
-  const float (*qs)[D];
+  const float (*qs)[D];        // scaled queries, in shared memory
   float m[G], l[G], acc[G][4];
 
+  const T* q;
+  static constexpr int kShare = G * D * 4;
   __device__ __forceinline__ void init(__half*, int) {}
-  __device__ __forceinline__ void load(const T*, int) {}
-  __device__ __forceinline__ void begin(const float (*qs_)[D], int) {
-    qs = qs_;
+  __device__ __forceinline__ void load(const T* q_, int) { q = q_; }
+  __device__ __forceinline__ void prepare(int) {}
+  __device__ __forceinline__ void share(void* to, int lane) const {
+    for (int i = lane; i < G * D; i += 32) reinterpret_cast<float*>(to)[i] = q[i] * (kLog2e / sqrtf((float)D));
+  }
+  __device__ __forceinline__ void fetch(const void* from, int) { qs = reinterpret_cast<const float(*)[D]>(from); }
+  __device__ __forceinline__ void reset() {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       m[g] = -INFINITY;
@@ -228,7 +235,8 @@ struct PageWarp<bf16, D, G> {
       raw[b] = g < G ? *reinterpret_cast<const uint4*>(q + g * D + b * 32 + t * 8) : make_uint4(0, 0, 0, 0);
   }
 
-  __device__ __forceinline__ void begin(const float (*)[D], int lane) {
+  // The unit's operands from `raw`.
+  __device__ __forceinline__ void prepare(int lane) {
     const int t = lane & 3;
     uint32_t top = 0;
 #pragma unroll
@@ -262,8 +270,6 @@ struct PageWarp<bf16, D, G> {
         sum += __shfl_xor_sync(0xffffffffu, sum, 1);
         sum += __shfl_xor_sync(0xffffffffu, sum, 2);
         c[k] = sum * (-8.f / 16777216.f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) O[b][0][i] = O[b][1][i] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
@@ -286,6 +292,31 @@ struct PageWarp<bf16, D, G> {
     }
     f0 = __shfl_sync(0xffffffffu, f, t * 8);
     f1 = __shfl_sync(0xffffffffu, f, t * 8 + 4);
+  }
+  // One warp prepares for the others (kShare bytes, 16-byte aligned).
+  static constexpr int kShare = (NB + 1) * 512;
+  __device__ __forceinline__ void share(void* to, int lane) const {
+    uint4* p = reinterpret_cast<uint4*>(to) + lane;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) p[b * 32] = make_uint4(qb[2 * b][0], qb[2 * b][1], qb[2 * b + 1][0], qb[2 * b + 1][1]);
+    p[NB * 32] = make_uint4(cb[0], cb[1], __float_as_uint(f0), __float_as_uint(f1));
+  }
+  __device__ __forceinline__ void fetch(const void* from, int lane) {
+    const uint4* p = reinterpret_cast<const uint4*>(from) + lane;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const uint4 v = p[b * 32];
+      qb[2 * b][0] = v.x; qb[2 * b][1] = v.y; qb[2 * b + 1][0] = v.z; qb[2 * b + 1][1] = v.w;
+    }
+    const uint4 v = p[NB * 32];
+    cb[0] = v.x; cb[1] = v.y;
+    f0 = __uint_as_float(v.z); f1 = __uint_as_float(v.w);
+  }
+  __device__ __forceinline__ void reset() {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) O[b][0][i] = O[b][1][i] = 0.f;
     m0 = m1 = kNoRef;
     r0 = r1 = 0.f;
     lim0 = lim1 = -INFINITY;
@@ -697,7 +728,7 @@ page_decode_kernel(const PageArgs<T> a) {
   constexpr int NW = kPdWarps, ST = kPdStages, RS = D + kPartPad;
   extern __shared__ __align__(128) unsigned char dsm[];
   float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
-  __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
+  __shared__ __align__(16) unsigned char s_q[PageWarp<T, D, G>::kShare];    // a unit's operands
   __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
   __shared__ float s_m[NW][G], s_l[NW][G], s_stat[G][2];
   __shared__ float s_new[3][G];   // the new row's logits, for the units of s_split and a whole one
@@ -818,20 +849,22 @@ page_decode_kernel(const PageArgs<T> a) {
     // microseconds later
     PageWarp<T, D, G> pw;
     pw.init(s_ones[warp], lane);
-    pw.load(a.q + (size_t)cp.u * G * D, lane);
+    const bool first_warp = warp == 0, last_warp = warp == NW - 1;
+    if (first_warp) pw.load(a.q + (size_t)cp.u * G * D, lane);
     PageRing<D, ST> pr;
     pr.start(a.pages, dsm + warp * ST * P::kBytes,
              reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc) + warp * ST, fill(), lane);
-    if (a.k_new != nullptr) {
-      u_first = cp.u;
-      const int n = (f1 - cp.at) / kUnitPages + 1;     // no more units than that begin before f1
-      if (n <= kPdLens) {
-        if (tid < n && cp.u + tid < a.units) s_len[tid] = a.len[cp.u + tid];
-        __syncthreads();
-        told = true;
-        if (warp == NW - 1) tell();
-      }
+    if (first_warp) {
+      pw.prepare(lane);
+      pw.share(s_q, lane);
     }
+    u_first = cp.u;
+    const int n = (f1 - cp.at) / kUnitPages + 1;       // no more units than that begin before f1
+    const bool keeps = a.k_new != nullptr && n <= kPdLens;
+    if (keeps && tid < n && cp.u + tid < a.units) s_len[tid] = a.len[cp.u + tid];
+    __syncthreads();
+    told = keeps;
+    if (told && last_warp) tell();
     pr.next = fill();
 
     for (int seg = f0; seg < f1;) {
@@ -840,12 +873,8 @@ page_decode_kernel(const PageArgs<T> a) {
       const int seg_end = min(f1, cp.end);
       const int first = cp.at / chunk, nsplit = (cp.end - 1) / chunk - first + 1;
       const int slot = (int)blockIdx.x == first ? 1 : 0;
-      if constexpr (sizeof(T) == 4) {
-        for (int i = tid; i < G * D; i += kPdThreads)
-          (&qs[0][0])[i] = to_f32(a.q[(size_t)u * G * D + i]) * (kLog2e / sqrtf((float)D));
-        __syncthreads();
-      }
-      pw.begin(reinterpret_cast<const float(*)[D]>(qs), lane);
+      pw.fetch(s_q, lane);
+      pw.reset();
       if (a.k_new != nullptr && nsplit == 1 && tid < 2)    // wanted at the unit's end
         prefetch_l2((tid == 0 ? a.k_new : a.v_new) + (size_t)u * D);
       static_assert(G <= NW, "a warp per query head");
@@ -854,11 +883,16 @@ page_decode_kernel(const PageArgs<T> a) {
         set_flag(a.flags, KVS_FLAG_TIMEOUT);
         lf = f1;
       }
-      if (seg_end < f1) pw.load(a.q + (size_t)(u + 1) * G * D, lane);
-      if (seg != f0) __syncthreads();              // the last unit's partials have been read
+      const bool more = seg_end < f1;
+      if (more && first_warp) pw.load(a.q + (size_t)(u + 1) * G * D, lane);
+      if (more || seg != f0) __syncthreads();      // the last unit's partials, this one's operands: read
       const int len = len_of(u);
       const int id = nsplit == 1 ? new_row(u, len, 2) : -1;
       pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
+      if (more && first_warp) {
+        pw.prepare(lane);
+        pw.share(s_q, lane);
+      }
       __syncthreads();
       if (tid < G * D / 4) {
         const int g = tid * 4 / D, c = tid * 4 % D;
@@ -900,13 +934,47 @@ page_decode_kernel(const PageArgs<T> a) {
       if (!s_last[i]) continue;
       // Sum the splits' rows: four columns a thread, the splits dealt out over NGRP threads for
       // each four, loads in batches.
-      constexpr int NU = S::kUnits, NGRP = S::kGroups, kBatch = 4;
+      constexpr int NU = S::kUnits, NGRP = S::kGroups, kBatch = 4, kFew = 6;
       const int4 sp = s_split[i];
       const int u = sp.x, np = sp.z;
       const int grp = tid / NU, unit = tid % NU, g = unit * 4 / D, c = unit * 4 % D;
       // slot 1 of the CTA the unit begins in, slot 0 of the others
       const float* rows = a.part + (size_t)sp.y * 2 * G * RS;
       auto row_of = [&](int s) { return rows + (2 * s + (s == 0 ? 1 : 0)) * G * RS; };
+      const int id = i == 0 ? new_id[0] : new_id[1];
+      if (np <= kFew) {
+        // few splits (the usual case): every thread weighs them for itself, one round trip
+        if (tid < NU) {
+          const int g = tid * 4 / D, c = tid * 4 % D;
+          float2 ml[kFew];
+          float4 v[kFew];
+#pragma unroll
+          for (int s = 0; s < kFew; ++s) {
+            ml[s] = make_float2(-INFINITY, 0.f);
+            v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s < np) {
+              ml[s] = __ldcg(reinterpret_cast<const float2*>(row_of(s) + g * RS + D));
+              v[s] = __ldcg(reinterpret_cast<const float4*>(row_of(s) + g * RS + c));
+            }
+          }
+          float M = -INFINITY, Ls = 0.f;
+#pragma unroll
+          for (int s = 0; s < kFew; ++s) M = fmaxf(M, ml[s].x);
+          float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int s = 0; s < kFew; ++s) {
+            const float f = part_weight(ml[s].x, ml[s].y, M);
+            Ls = fmaf(ml[s].y, f, Ls);
+            A.x = fmaf(v[s].x, f, A.x); A.y = fmaf(v[s].y, f, A.y);
+            A.z = fmaf(v[s].z, f, A.z); A.w = fmaf(v[s].w, f, A.w);
+          }
+          finish_columns<T>(A, M, Ls, id >= 0 ? s_new[i][g] : -INFINITY, a.v_new + (size_t)u * D + c,
+                            a.out + (size_t)u * G * D + tid * 4);
+        }
+        append(u, sp.w, id);
+        if (tid == 0) a.counters[u] = 0;
+        continue;
+      }
       float* fac = s_acc;                          // [G][np]
       float4 v[kBatch];
       auto load_batch = [&](int s0) {
@@ -916,7 +984,6 @@ page_decode_kernel(const PageArgs<T> a) {
             v[j] = __ldcg(reinterpret_cast<const float4*>(row_of(s0 + j * NGRP) + g * RS + c));
       };
       load_batch(grp);                             // with the factors' loads: one round trip for both
-      const int id = i == 0 ? new_id[0] : new_id[1];
       if (warp < G) {
         constexpr int kPer = (kPageDecodeCtas + 31) / 32;
         float2 ml[kPer];
@@ -994,7 +1061,7 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   extern __shared__ __align__(128) unsigned char dsm[];
   float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
   float* s_sum = reinterpret_cast<float*>(dsm + S::kRing + S::kAcc);        // [G][D], read by peers
-  __shared__ __align__(16) float qs[G][sizeof(T) == 4 ? D : 4];             // fp32: scaled queries
+  __shared__ __align__(16) float s_q[sizeof(T) == 4 ? G * D : 4];           // fp32: PageWarp::share
   __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
   __shared__ float s_m[NW][G], s_l[NW][G], s_new[G];
   __shared__ __align__(8) float s_ml[G][2];                                 // read by peers
@@ -1027,12 +1094,14 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   pr.start(a.pages, dsm + warp * ST * P::kBytes,
            reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc + S::kSum) + warp * ST, entry(), lane);
   pr.next = fill();
+  // (every warp for itself: there is one unit, and a barrier would cost more)
+  pw.prepare(lane);
   if constexpr (sizeof(T) == 4) {
-    for (int i = tid; i < G * D; i += NW * 32)
-      (&qs[0][0])[i] = to_f32(a.q[(size_t)u * G * D + i]) * (kLog2e / sqrtf((float)D));
+    if (warp == 0) pw.share(s_q, lane);
     __syncthreads();
+    pw.fetch(s_q, lane);
   }
-  pw.begin(reinterpret_cast<const float(*)[D]>(qs), lane);
+  pw.reset();
   const int new_id = a.k_new != nullptr ? a.new_page(u, len) : -1;
   if (new_id >= 0 && warp < G) {
     const float sn = new_logit<T, D, G>(a, u, warp, lane);
