@@ -63,7 +63,19 @@ struct PageClusterShape {
   static constexpr int kSmem = kRing + kAcc + kSum + kPcWarps * kPcStages * 8;
 };
 
-static bool use_cluster(int C, int max_pages) { return C >= 8 && max_pages <= 128 * C; }
+// A cluster per unit, or the split kernel? The cluster's launch costs 4 to 5 us less (no numbering,
+// no round trip to the workspace), but the longest unit sets its time, and the host knows only
+// how many pages a unit may have. Measured (us, G = 4, d = 128, equal lengths; cluster | split):
+//   8 units (C = 10)   2048 rows  6.2 |  9.9   16384 rows 10.9 | 14.6   65536 rows 26.2 | 27.9
+//   32 units (C = 4)   2048 rows  7.2 | 11.2   16384 rows 19.7 | 24.3
+//   64 units (C = 2)    512 rows  6.9 | 10.0    8192 rows 20.2 | 24.1
+// A lone full unit of 64 C pages among empty ones takes the cluster 12 us, the split kernel 9 or more; of
+// 128 C pages 18 us, which is taken for the few units that C >= 8 means, as they are mostly the heads
+// of one sequence.
+static bool use_cluster(int C, int max_pages) { return C >= 2 && max_pages <= (C >= 8 ? 128 : 64) * C; }
+
+// How many pages more than the mean the longest unit may have in a CTA for a split by units.
+constexpr int kByUnit = 40;
 
 // Places of a unit in the numbering: its pages, and some for the work at its end (an empty unit
 // has a place, so that a CTA finishes it).
@@ -78,15 +90,16 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 // others), reset() starts a unit, take() adds the first nval rows of a page, end() writes the partial output
 // [G][D] and (m, l) per query head (log2 domain; m is a reference, not always the maximum).
 
-// fp32: CUDA cores, every product and sum in fp32. Logits with a lane per row, values with a lane
-// per channel quad. Not tuned: the fp32 cache is the accuracy path, and this kernel stays within
-// an fp32 softmax attention's own error.
+// fp32: CUDA cores, every product and sum in fp32 (two at a time where they come in pairs), so
+// that it stays within an fp32 softmax attention's own error. Logits with a lane per row, values
+// with a lane per channel quad. Bound by the fp32 pipe.
 template <typename T, int D, int G>
 struct PageWarp {
   using P = PageLayout<D>;
   static constexpr int QL = D / 4, RPS = 32 / QL;       // lanes per row of V, rows at a time
   const float (*qs)[D];        // scaled queries, in shared memory
-  float m[G], l[G], acc[G][4];
+  float m[G], l[G];
+  float2 acc[G][2];
 
   const T* q;
   static constexpr int kShare = G * D * 4;
@@ -101,7 +114,8 @@ struct PageWarp {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       m[g] = -INFINITY;
-      l[g] = acc[g][0] = acc[g][1] = acc[g][2] = acc[g][3] = 0.f;
+      l[g] = 0.f;
+      acc[g][0] = acc[g][1] = make_float2(0.f, 0.f);
     }
   }
 
@@ -114,50 +128,65 @@ struct PageWarp {
       const uint4 w4 = *reinterpret_cast<const uint4*>(pg + P::k_code(b, lane));
       const float s = __half2float(*reinterpret_cast<const __half*>(pg + P::k_scale(b, lane)));
       const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-      float y[G];
+      float2 y[G];
 #pragma unroll
-      for (int g = 0; g < G; ++g) y[g] = 0.f;
+      for (int g = 0; g < G; ++g) y[g] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float k[8];
-        dequantise8(w[i], 1.f, k);
+        centred8(w[i], k);
 #pragma unroll
         for (int g = 0; g < G; ++g)
 #pragma unroll
-          for (int c = 0; c < 8; ++c) y[g] = fmaf(qs[g][b * 32 + i * 8 + c], k[c], y[g]);
+          for (int c = 0; c < 8; c += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(&qs[g][b * 32 + i * 8 + c]);
+            y[g] = ffma2(make_float2(v.x, v.y), make_float2(k[c], k[c + 1]), y[g]);
+            y[g] = ffma2(make_float2(v.z, v.w), make_float2(k[c + 2], k[c + 3]), y[g]);
+          }
       }
 #pragma unroll
-      for (int g = 0; g < G; ++g) x[g] = fmaf(y[g], s, x[g]);
+      for (int g = 0; g < G; ++g) x[g] = fmaf(y[g].x + y[g].y, s, x[g]);
     }
     const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane)) * kLog2e;
     float p[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       const float xg = lane < nval ? x[g] + ln : -INFINITY;
-      const float M = fmaxf(m[g], warp_max(xg));
-      const float base = M == -INFINITY ? 0.f : M;
-      const float f = exp2f(m[g] - base);
-      p[g] = exp2f(xg - base);
-      l[g] = fmaf(l[g], f, p[g]);
-      m[g] = M;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[g][c] *= f;
-    }
-    const int quad = lane % QL, b = quad / 8;
-    for (int r0 = 0; r0 < nval; r0 += RPS) {
-      const int r = r0 + lane / QL;
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(pg + P::v_piece(b, r, quad % 8));
-      float s = __half2float(*reinterpret_cast<const __half*>(pg + P::v_scale(b, r)));
-      if (r >= nval) s = 0.f;                  // whatever the rest of the page holds
-      float v[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) v[c] = (float)((int)(w >> (4 * c) & 15u) - 8) * s;
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        const float pr = __shfl_sync(0xffffffffu, p[g], r);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) acc[g][c] = fmaf(pr, v[c], acc[g][c]);
+      if (__any_sync(0xffffffffu, xg > m[g])) {      // a new maximum: rare after the first pages
+        const float M = fmaxf(m[g], warp_max(xg));
+        const float f = exp2f(m[g] - M);
+        l[g] *= f;
+        acc[g][0].x *= f; acc[g][0].y *= f; acc[g][1].x *= f; acc[g][1].y *= f;
+        m[g] = M;
       }
+      p[g] = exp2f(xg - (m[g] == -INFINITY ? 0.f : m[g]));
+      l[g] += p[g];
+    }
+    // a pair of rows at a time: one word holds the quad's channels of both
+    const int quad = lane % QL, b = quad / 8;
+#pragma unroll 2
+    for (int r0 = 0; r0 < nval; r0 += 2 * RPS) {
+      const int r = r0 + 2 * (lane / QL);
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r, quad % 8));
+      float2 s = __half22float2(*reinterpret_cast<const __half2*>(pg + P::v_scale(b, r)));
+      if (r >= nval) s.x = 0.f;                      // whatever the rest of the page holds
+      if (r + 1 >= nval) s.y = 0.f;
+      float v[8];
+      centred8(w, v);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        v[c] *= s.x;
+        v[4 + c] *= s.y;
+      }
+#pragma unroll
+      for (int g = 0; g < G; ++g)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float pr = __shfl_sync(0xffffffffu, p[g], r + i);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            acc[g][c] = ffma2(make_float2(pr, pr), make_float2(v[4 * i + 2 * c], v[4 * i + 2 * c + 1]), acc[g][c]);
+        }
     }
   }
 
@@ -169,12 +198,14 @@ struct PageWarp {
         sm[g] = m[g];
         sl[g] = ls;
       }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (RPS == 2) acc[g][c] += __shfl_xor_sync(0xffffffffu, acc[g][c], 16);
-      if (lane < QL)
-        *reinterpret_cast<float4*>(sa + g * D + lane * 4) =
-            make_float4(acc[g][0], acc[g][1], acc[g][2], acc[g][3]);
+      float4 v = make_float4(acc[g][0].x, acc[g][0].y, acc[g][1].x, acc[g][1].y);
+      if (RPS == 2) {
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
+        v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, 16);
+        v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+      }
+      if (lane < QL) *reinterpret_cast<float4*>(sa + g * D + lane * 4) = v;
     }
   }
 };
@@ -743,21 +774,38 @@ page_decode_kernel(const PageArgs<T> a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid < 2) s_split[tid].x = -1;
 
-  // The numbering: total pages, and the unit and page this CTA starts with. Every warp works it
-  // out for itself, so no barrier comes before the first copies. The host keeps the total below
-  // 2^31.
-  uint32_t sum = 0;
+  // Every warp reads all lengths and settles for itself what this CTA does, so no barrier comes
+  // before the first copies. The host keeps the total below 2^31.
+  uint32_t sum = 0, most = 0;
 #pragma unroll 4
   for (int u = lane; u < a.units; u += 32) {
     const int L = a.len[u];
     if (L != a.legal(L) && blockIdx.x == 0 && warp == 0) set_flag(a.flags, KVS_FLAG_BAD_LENGTH);
     sum += unit_span(a.legal(L));
+    most = max(most, (uint32_t)pages_of(a.legal(L)));
   }
   const int total = (int)__reduce_add_sync(0xffffffffu, sum);
+  const int longest = (int)__reduce_max_sync(0xffffffffu, most);
+  // Two ways to split the pages. Even runs of the numbering: the same work for every CTA, but a
+  // unit begins and ends anywhere in a CTA. Or `per_unit` CTAs for each unit, which saves the
+  // boundaries (about 8 us of a launch, 40 pages of a CTA) and costs what the longest unit is
+  // longer than the mean.
+  const int per_unit = (int)gridDim.x / a.units;
+  const bool by_unit = per_unit > 0 && (longest + per_unit - 1) / per_unit <= total / (int)gridDim.x + kByUnit;
   // at least one page per warp of a CTA: short caches gain nothing from more partial rows
   const int chunk = max(NW, (total + (int)gridDim.x - 1) / (int)gridDim.x);
-  const int f0 = (int)min((long long)total, (long long)blockIdx.x * chunk);
-  const int f1 = (int)min((long long)total, (long long)f0 + chunk);
+  int f0, f1, part = 0, parts = 1;                     // this CTA's places
+  if (by_unit) {
+    const int u = blockIdx.x / per_unit;
+    part = blockIdx.x % per_unit;
+    const int np = u < a.units ? pages_of(a.legal(a.len[u])) : 0;
+    parts = max(1, min(per_unit, np / (2 * NW)));      // two pages per warp at least
+    f0 = (int)((long long)np * part / parts);
+    f1 = u < a.units && part < parts ? max(f0 + 1, (int)((long long)np * (part + 1) / parts)) : f0;
+  } else {
+    f0 = (int)min((long long)total, (long long)blockIdx.x * chunk);
+    f1 = (int)min((long long)total, (long long)f0 + chunk);
+  }
   // Lengths move on when every CTA has read them, so this CTA says when it has: once the ones
   // of its own units are in shared memory, while the first pages are on their way. (A CTA with
   // more units than fit there reads on from memory, and says so at its end.)
@@ -806,7 +854,12 @@ page_decode_kernel(const PageArgs<T> a) {
       }
     };
     Place cp;
-    {
+    if (by_unit) {
+      cp.u = blockIdx.x / per_unit;
+      cp.L = a.legal(a.len[cp.u]);
+      cp.at = 0;
+      cp.end = unit_span(cp.L);
+    } else {
       int base = 0, acc = 0, w, n;                 // the 32 units that page f0 falls among
       for (;; base += 32, acc += n) {
         w = base + lane < a.units ? unit_span(a.legal(a.len[base + lane])) : 0;
@@ -824,6 +877,13 @@ page_decode_kernel(const PageArgs<T> a) {
       cp.L = a.legal(a.len[cp.u]);
       cp.end = acc + __shfl_sync(0xffffffffu, inc, who);
       cp.at = cp.end - unit_span(cp.L);
+    }
+
+    // a run that begins in the padding of a unit leaves that unit to others
+    auto live_end = [&](const Place& p) { return p.at + max(1, pages_of(p.L)); };
+    if (f0 >= live_end(cp)) {
+      f0 = min(f1, cp.end);
+      if (f0 < f1) move_to(cp, f0);
     }
 
     // This warp's pages are f0 + warp, f0 + warp + NW, ...
@@ -859,7 +919,7 @@ page_decode_kernel(const PageArgs<T> a) {
       pw.share(s_q, lane);
     }
     u_first = cp.u;
-    const int n = (f1 - cp.at) / kUnitPages + 1;       // no more units than that begin before f1
+    const int n = by_unit ? 1 : (f1 - cp.at) / kUnitPages + 1;     // no more units than that begin before f1
     const bool keeps = a.k_new != nullptr && n <= kPdLens;
     if (keeps && tid < n && cp.u + tid < a.units) s_len[tid] = a.len[cp.u + tid];
     __syncthreads();
@@ -871,7 +931,8 @@ page_decode_kernel(const PageArgs<T> a) {
       move_to(cp, seg);
       const int u = cp.u;
       const int seg_end = min(f1, cp.end);
-      const int first = cp.at / chunk, nsplit = (cp.end - 1) / chunk - first + 1;
+      const int first = by_unit ? (int)blockIdx.x - part : cp.at / chunk;
+      const int nsplit = by_unit ? parts : (live_end(cp) - 1) / chunk - first + 1;
       const int slot = (int)blockIdx.x == first ? 1 : 0;
       pw.fetch(s_q, lane);
       pw.reset();
@@ -1230,7 +1291,7 @@ static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_pa
                          reinterpret_cast<float*>(ws + Ly.part), reinterpret_cast<int32_t*>(ws)};
   count_launches(1);
   const int C = page_cluster_size<T, D, G>(units);
-  if (C >= 2 && use_cluster(C, pool.max_pages)) {
+  if (use_cluster(C, pool.max_pages)) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C, units);
     cfg.blockDim = dim3(kPcWarps * 32);

@@ -145,13 +145,29 @@ __device__ __forceinline__ uint32_t quantise_lane(const Raw8<T>& raw, uint32_t& 
   return quantise8<T>(x, sb);
 }
 
-// The 8 channels of a word of codes at scale s.
-__device__ __forceinline__ void dequantise8(uint32_t w, float s, float* x) {
+// c = u - 8 of the 8 codes of a word, low nibble first. A code put into the low bits of 2^23 adds
+// u 16^j to it, and one fused multiply-add takes 2^23 and 8 off again, exactly; an integer
+// conversion would run at a quarter of the rate.
+__device__ __forceinline__ void centred8(uint32_t w, float* c) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (float)((int)((w >> (4 * i)) & 15u) - 8) * s;
+  for (int i = 0; i < 8; ++i) {
+    const int j = i & 3;
+    const uint32_t v = i < 4 ? w : w >> 16;
+    const float f = __uint_as_float((v & (15u << (4 * j))) | 0x4b000000u);
+    c[i] = fmaf(f, 1.f / (float)(1 << (4 * j)), -(8388608.f / (float)(1 << (4 * j)) + 8.f));
+  }
 }
 
-// Pages that `rows` rows fill; the decode counts an empty unit as one page.
-__host__ __device__ __forceinline__ int pages_of(int rows) { return (rows + kPageRows - 1) / kPageRows; }
+// The 8 channels of a word of codes at scale s.
+__device__ __forceinline__ void dequantise8(uint32_t w, float s, float* x) {
+  centred8(w, x);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= s;
+}
+
+// Pages that `rows` >= 0 rows fill (no overflow for the largest int).
+__host__ __device__ __forceinline__ int pages_of(int rows) {
+  return (int)(((unsigned)rows + kPageRows - 1) / kPageRows);
+}
 
 }  // namespace kvs

@@ -394,6 +394,74 @@ def test_decode_of_many_short_units(kvs, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens", [[6000] + [k % 40 for k in range(63)],          # one long among 64
+                                  [k * 37 % 90 for k in range(149)] + [1900],    # more units than half the CTAs
+                                  [0, 0, 3, 0, 1200, 0] * 60])
+def test_decode_of_units_that_differ_much(kvs, dtype, lens):
+    c = Cache(kvs, 1, len(lens), 2, 64, lens, dtype, seed=4, wide=2000)
+    q, kn, vn = c.random(1, 2 * len(lens), 64), c.random(1, len(lens), 64), c.random(1, len(lens), 64)
+    c.check(q, c.step(q))
+    c.check(q, c.step(q, kn, vn), kn, vn)
+    c.append(kn, vn)
+    assert kvs.device_flags(c.ws) == 0
+
+
+def long_cache(kvs, dtype, d, G, rows, n_pages, first, wide=0):
+    """One unit of `rows` rows in pages from `first` on, stored from random rows; and its rows as
+    the pages hold them."""
+    g = torch.Generator(device=DEV).manual_seed(rows)
+    n = -(-rows // PAGE)
+    pages = torch.empty(n_pages, kvs.page_bytes(d), dtype=torch.uint8, device=DEV)
+    table = torch.full((1, n + 1 + wide), -1, dtype=torch.int32, device=DEV)
+    table[0, :n] = first + torch.randperm(n, generator=g, device=DEV).to(torch.int32)
+    pool = kvs.page_pool(pages, table)
+    desc = kvs.make_desc(1, 1, G, d, rows + rows % 2, dtype)
+    ws = kvs.workspace(desc, ops=(kvs.OP_PAGES,))
+    t = torch.arange(desc.T_cap, device=DEV)
+    slots = torch.where(t < rows, table[0].repeat_interleave(PAGE)[:desc.T_cap] * PAGE + t % PAGE, -1)
+    slots = slots.to(torch.int32).view(1, 1, -1)
+    K, V = (torch.randn(1, 1, desc.T_cap, d, generator=g, device=DEV).to(dtype) for _ in range(2))
+    logn = torch.rand(1, 1, desc.T_cap, generator=g, device=DEV)
+    kvs.page_store(desc, K, V, logn, slots, pool, ws)
+    f32 = kvs.make_desc(1, 1, G, d, desc.T_cap, torch.float32)
+    K, V = torch.zeros(1, 1, desc.T_cap, d, device=DEV), torch.zeros(1, 1, desc.T_cap, d, device=DEV)
+    kvs.page_load(f32, pool, slots, K, V, None, ws)
+    q = (2 * torch.randn(1, G, d, generator=g, device=DEV)).to(dtype)
+    lens = torch.tensor([rows], dtype=torch.int32, device=DEV)
+    out = torch.empty_like(q)
+    kvs.page_decode_attn(desc, q, pool, lens, out, ws)
+    k, v = K[0, 0, :rows].double(), V[0, 0, :rows].double()
+    w = torch.softmax(q[0].double() @ k.T / d ** 0.5 + logn[0, 0, :rows].double(), -1)
+    s = v.abs().view(rows, -1, 32).amax(-1).repeat_interleave(32, 1) / 7      # (no scale is subnormal here)
+    x = float((q[0].double().abs() @ k.abs().T).max()) / d ** 0.5 + 1
+    size, want = w @ v.abs(), w @ v
+    bound = (2 * (d + 6) * 2.0 ** -24 * x + (rows + 16) * 2.0 ** -24 + 2.0 ** -21) * size + 2.0 ** -24 * want.abs()
+    if dtype == torch.bfloat16:
+        bound = bound + 2.0 ** -11 * (size + want.abs() + 15 * (w @ s)) + 2.0 ** -8 * want.abs() + rows * 2.0 ** -27
+    err = (out[0].double() - want).abs()
+    assert bool((err <= bound).all()), float((err / bound).max())
+    assert kvs.device_flags(ws) == 0
+
+
+@pytest.mark.parametrize("dtype,d,G,rows,wide", [
+    (torch.bfloat16, 64, 4, 300001, 0),             # more pages per warp than one list holds
+    (torch.bfloat16, 128, 1, 40000, 0),
+    (torch.float32, 64, 2, 90017, 0),
+    (torch.bfloat16, 64, 1, 2600011, 0),            # the same for the split kernel
+    (torch.bfloat16, 128, 4, 100003, 9000)])
+def test_decode_of_very_long_units(kvs, dtype, d, G, rows, wide):
+    n = -(-rows // PAGE)
+    long_cache(kvs, dtype, d, G, rows, n + 5, 3, wide)
+
+
+def test_pages_past_four_gigabytes(kvs):
+    n = 2 ** 32 // kvs.page_bytes(128) + 100
+    if torch.cuda.mem_get_info()[0] < 8 << 30:
+        pytest.skip("needs 8 GB of device memory")
+    long_cache(kvs, torch.bfloat16, 128, 4, 3001, n, n - 97)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_decode_steps_cross_a_page(kvs, dtype, wide):
     c = Cache(kvs, 1, 4, 4, 128, [0, 30, 31, 61], dtype, seed=5, room=5, wide=wide)
     for _ in range(5):
