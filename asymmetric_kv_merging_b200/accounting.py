@@ -62,3 +62,26 @@ def prefill_chunk_bytes(L, n, budget, sink, W, head_dim, elem_bytes, fused=True)
         length -= R
         rounds += 1
     return total, rounds
+
+
+PAGE_ROWS = 32
+
+
+def page_bytes(head_dim):
+    """Bytes of a page of the 4-bit paged cache: for each of 32 rows the codes of K and V, a
+    half-precision scale per 32 channels of each, and an fp32 log-count."""
+    return PAGE_ROWS * (int(head_dim) + 2 * int(head_dim) // 32 * 2 + 4)
+
+
+def page_decode_bytes(n_rows, n_units, group, head_dim, elem_bytes):
+    """Algorithmic bytes of one decode step over the paged cache: every row of the units once,
+    the page numbers and lengths, the queries and the output."""
+    rows = int(n_rows) * page_bytes(head_dim) / PAGE_ROWS + 4 * int(n_rows) / PAGE_ROWS
+    return rows + int(n_units) * (4 + 2 * int(group) * int(head_dim) * int(elem_bytes))
+
+
+def page_store_bytes(n_rows, head_dim, elem_bytes):
+    """Algorithmic bytes of moving rows between a cache and pages, one way: the rows with their
+    log-counts, their slots, and the pages."""
+    row = 2 * int(head_dim) * int(elem_bytes) + 4 + 4
+    return int(n_rows) * (row + page_bytes(head_dim) / PAGE_ROWS)

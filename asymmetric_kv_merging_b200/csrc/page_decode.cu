@@ -4,15 +4,26 @@
 // §数学主线三) with the log-count bias of merged rows, over rows held in pages (pages.cuh):
 //   x_t = q . k_t / sqrt(d) + logn_t,  out = sum_t 2^(x_t log2 e - M) v_t / sum_t 2^(x_t log2 e - M)
 //
-// Work split. The pages of all units (KV heads of all sequences) are numbered one unit after
-// another, and CTA i takes pages [i c, (i + 1) c): lengths are ragged and known on the device
-// only, so every CTA sums them up for itself. A unit that lies in one CTA is finished there; one
-// that spans several gets a partial row per CTA in the workspace, and the last of them to arrive
-// (a counter per unit) combines. No CTA waits for another.
-//
 // A page is one contiguous block, so a single bulk copy (untiled, no tensor map) brings it into
 // the ring of the warp that works on it; each warp issues its own copies and needs no other
-// warp until the end of a unit.
+// warp until the end of a unit. Two kernels share the work on a page (PageWarp, PageRing):
+//  - split kernel: lengths are ragged and known on the device only, so every CTA sums them up for
+//    itself. The pages of all units (KV heads of all sequences) are numbered one unit after
+//    another and dealt out in even runs, or a fixed number of CTAs goes to each unit. A unit that
+//    lies in one CTA is finished there; one that spans several gets a partial row per CTA in the
+//    workspace, and the last of them to arrive (a counter per unit) combines. No CTA waits for
+//    another.
+//  - cluster kernel: one thread-block cluster per unit, combined in distributed shared memory.
+//
+// Measured on one B200 (G = 4, d = 128, bf16; device time of back-to-back launches over inputs
+// larger than L2; bytes are 148 a row):
+//   cluster   8 units x  2048 rows    6.2 us (2.4 MB: launch, three round trips and the combine)
+//             8 units x 16384 rows   10.9 us, 1.8 TB/s
+//             8 units x 32768 rows   16.6 us, 2.3 TB/s (80 SMs: ten CTAs are the largest cluster
+//                                    of which eight fit the GPU at once)
+//   split    64 units x 11K..22K     38.3 us, 4.1 TB/s = 0.62 of the measured copy peak
+//           128 units x 1K..8K       29.0 us, 3.0 TB/s
+// The same kernels without the arithmetic take 4.1, 5.7, 10.2, 31.5 and 23.1 us.
 #include <map>
 #include <mutex>
 #include <utility>
@@ -25,6 +36,9 @@
 
 namespace kvs {
 
+// Split kernel: two CTAs of 8 warps an SM (128 registers a thread, 100 to 115 KB of shared memory),
+// so that one streams while the other ends a unit; two stages a warp are 150 KB of copies in
+// flight per SM (a prefetch of the pages after those into L2 measured 3% to 15% slower).
 constexpr int kPdWarps = 8;
 constexpr int kPdThreads = kPdWarps * 32;
 constexpr int kPdStages = 2;
@@ -52,6 +66,7 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) {
   return l != 0.f ? ex2_ftz(m - M) : 0.f;
 }
 
+// Cluster kernel: one CTA of 16 warps an SM (all of its clusters have to fit at once).
 constexpr int kPcWarps = 16;
 constexpr int kPcStages = 2;
 
@@ -69,16 +84,20 @@ struct PageClusterShape {
 //   8 units (C = 10)   2048 rows  6.2 |  9.9   16384 rows 10.9 | 14.6   65536 rows 26.2 | 27.9
 //   32 units (C = 4)   2048 rows  7.2 | 11.2   16384 rows 19.7 | 24.3
 //   64 units (C = 2)    512 rows  6.9 | 10.0    8192 rows 20.2 | 24.1
-// A lone full unit of 64 C pages among empty ones takes the cluster 12 us, the split kernel 9 or more; of
-// 128 C pages 18 us, which is taken for the few units that C >= 8 means, as they are mostly the heads
-// of one sequence.
+// A lone full unit of 64 C pages among empty ones takes the cluster 12 us and the split kernel 9 to
+// 12; one of 128 C pages 18 us, a risk that is taken for the few units that C >= 8 means, as they are
+// mostly the heads of one sequence.
 static bool use_cluster(int C, int max_pages) { return C >= 2 && max_pages <= (C >= 8 ? 128 : 64) * C; }
 
 // How many pages more than the mean the longest unit may have in a CTA for a split by units.
+// Measured (us, equal lengths; by units | even runs): 16 units x 8192 rows 12.5 | 15.4, 128 x 2048
+// 17.5 | 20.0, 256 x 512 11.5 | 17.0, 64 x 16384 38.1 | 37.6; on the ragged batches of 64 and 128
+// units, which the rule leaves to the even runs, 45.7 | 38.3 and 37.3 | 29.2.
 constexpr int kByUnit = 40;
 
-// Places of a unit in the numbering: its pages, and some for the work at its end (an empty unit
-// has a place, so that a CTA finishes it).
+// Places of a unit in the numbering: its pages, and some padding for the work at its end (an
+// empty unit has a place, so that a CTA finishes it). Measured on the ragged batches of 64 and 128
+// units: 4 places 40.4 and 31.4 us, 8: 40.0 and 30.8, 12: 39.4 and 30.1, 24: 39.5 and 30.6.
 constexpr int kUnitPages = 12;
 __device__ __forceinline__ int unit_span(int L) { return pages_of(L) + kUnitPages; }
 
@@ -225,11 +244,22 @@ struct PageWarp {
 //   V: the block's scale goes onto the weights (B), w = half(half(p) scale), and
 //      sum_t (u - 8) scale p = sum_t u w - 8 sum_t scale p. The second sum is one MMA for all
 //      blocks, with the scales as A and the weights half(p) as B (and a row of ones, for the sum
-//      of the weights); it does not see the rounding of w, which therefore counts on |u| <= 15 instead of |u - 8| <= 7. Of two channels in a
-//      byte one is summed alone and the other as u + 16 u'; the difference is taken at the end.
+//      of the weights); it does not see the rounding of w, which therefore counts on |u| <= 15
+//      instead of |u - 8| <= 7. Of two channels in a byte one is summed alone and the other as
+//      u + 16 u'; the difference is taken at the end.
 // p and w are rounded to half (2^-11 each); the reference m keeps p scale <= 2^15 and the largest
 // p at 2^7 (over scales above 1) or more when it was set, so weights down to 2^-21 of the largest
 // stay normal halves, and below that the error is at most 2^-25 / 2^7 of it.
+//
+// What bounds it: 450 instructions a page (32 rows, d = 128), of which 211 on the integer pipe,
+// which takes one every other cycle, and 36 MMAs of 8 cycles on the tensor pipe of the legacy
+// MMAs; the two hardly overlap. About 197 cycles a page and SM, from 12 warps an SM on (20 warps
+// at 96 registers gain nothing), where an SM's share of the copy peak brings a page in 203: both
+// bounds at once. Converting the codes to half instead costs 8 conversions and 8 products a word
+// where this takes 4 or 5 integer operations; unpacking for tcgen05 would have to write every
+// unpacked register to tensor memory first. Fragments by ldmatrix instead of 27 more loads, the
+// reference inside the sums and the weight sums by MMA took the page from 507 to 450.
+
 // The reference before the first row: below every logit, and finite, so that masked rows (-inf)
 // have a weight of 0 against it.
 constexpr float kNoRef = -1e30f;

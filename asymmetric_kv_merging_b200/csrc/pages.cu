@@ -105,8 +105,11 @@ page_scan_kernel(const int32_t* __restrict__ rows, const int32_t* __restrict__ h
 // stack that is read is also written, and no CTA waits for another; what other CTAs still read
 // (the held counts, and the table entries of given pages if a slot map has to find those) is
 // written by the last CTA to finish.
-// Small: latency-bound (a launch, the lengths, a page number, its slot). Large: the slot map's
-// writes. Sums and searches per CTA cost less than a second launch would.
+// Latency-bound throughout (a launch, the lengths, a page number, its slot): 128 units that give
+// all pages back and take 18000 others with a slot map of a million rows, 15 us for the two calls
+// (the same bytes take 0.7 us); 8 rows more for each of 128 units, 4.9 us a call. Sums and searches
+// in every CTA cost less than a second launch would; one CTA for the page numbers and a second
+// launch for the slots took 29 and 6.4 us.
 template <bool kLocal>
 __global__ void __launch_bounds__(kAssignThreads)
 page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* table,
@@ -248,7 +251,10 @@ cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32
 // A warp takes 8 consecutive rows, lane l channels 8 (l mod 4) .. of row l / 4 of one block of 32
 // channels after another. Codes of consecutive slots are then whole 128-byte lines (8 rows of 16
 // bytes; 4 pairs of 32), the maximum of a block is two shuffles away, and a lane has all the
-// loads of its row (8 of 16 bytes at d = 128 in bf16) in flight together.
+// loads of its row (8 of 16 bytes at d = 128 in bf16) in flight together. 262144 rows of d = 128 in
+// bf16 (175 MB of rows and pages): stored in 33.2 us, 5.3 TB/s = 0.81 of the measured copy peak, and
+// loaded in 30 us, 0.89. The store is near its issue rate too (79% of the slots): with two rows a
+// warp step and the codes masked and shifted into place one by one it took 61 us, the load 37.
 constexpr int kRowThreads = 256;
 constexpr int kRowsPerWarp = 8;
 constexpr int kRowsPerBlock = kRowThreads / 32 * kRowsPerWarp;

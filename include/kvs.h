@@ -418,12 +418,16 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * attend gets zeros. Rows whose page number is outside the pool are skipped
  * (KVS_FLAG_BAD_PAGE). T_cap of desc is not used. Two units may share a page that neither
  * appends to.
+ * Rounding: fp32 descriptors compute in fp32 throughout; with bf16 the softmax weights are
+ * rounded to half precision (2^-11), alone and times a row's scale.
  * In:  q [B,H_q,d]; pool; len [B*H_kv], 0 <= len <= 32 max_pages;
  *      B * H_kv * (max_pages + 64) < 2^31.
  * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
  * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes; its counters must be zero at
  * the first call (each call leaves them zero). Make the first call for a device outside any
- * stream capture (it sets a kernel attribute). Launched with programmatic stream
+ * stream capture (it sets kernel attributes and asks the occupancy calculator). Few units
+ * with short tables are decoded by a cluster of CTAs each, other calls by CTAs that split all
+ * pages among them; the same call gives the same bits. Launched with programmatic stream
  * serialisation, in plain stream order, as kvs_decode_attn is.
  */
 kvs_status kvs_page_decode_attn(const kvs_cache_desc* desc, const void* q,

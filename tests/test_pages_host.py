@@ -147,3 +147,14 @@ def test_checker_pages_round_trip():
                 seen[[o, o + 1]] += 1
             seen[ln:ln + 4] += 1
         assert np.all(seen == 1)
+
+
+def test_accounting_of_pages(kvs):
+    from asymmetric_kv_merging_b200 import accounting
+    for d in (64, 128):
+        assert accounting.page_bytes(d) == kvs.page_bytes(d) == ref.page_bytes(d)
+    # 148 bytes a row against 516 at d = 128 in bf16
+    assert accounting.page_bytes(128) / 32 == 148
+    assert accounting.decode_bytes_per_token(128, 2) == 516
+    assert accounting.page_decode_bytes(320, 2, 4, 128, 2) == 320 * 148 + 40 + 2 * (4 + 2048)
+    assert accounting.page_store_bytes(64, 64, 4) == 64 * (520 + 76)
