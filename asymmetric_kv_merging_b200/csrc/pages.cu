@@ -16,7 +16,7 @@ namespace kvs {
 // Page tables from lengths
 // ---------------------------------------------------------------------------
 
-constexpr int kAssignThreads = 512;
+constexpr int kAssignThreads = 256;
 constexpr int kAssignLocal = 4096;    // units whose offsets fit in shared memory (32 KB)
 
 struct UnitPages {
@@ -106,8 +106,8 @@ page_scan_kernel(const int32_t* __restrict__ rows, const int32_t* __restrict__ h
 // (the held counts, and the table entries of given pages if a slot map has to find those) is
 // written by the last CTA to finish.
 // Latency-bound throughout (a launch, the lengths, a page number, its slot): 128 units that give
-// all pages back and take 18000 others with a slot map of a million rows, 15 us for the two calls
-// (the same bytes take 0.7 us); 8 rows more for each of 128 units, 4.9 us a call. Sums and searches
+// all pages back and take 18000 others with a slot map of a million rows, 14 us for the two calls
+// (the same bytes take 0.7 us); 8 rows more for each of 128 units, 4.5 us a call. Sums and searches
 // in every CTA cost less than a second launch would; one CTA for the page numbers and a second
 // launch for the slots took 29 and 6.4 us.
 template <bool kLocal>
@@ -154,16 +154,20 @@ page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* tab
   for (long long i = gtid; i < taken - given; i += gsize) taken_at((int)i) = free_pages[top + i];
 
   if (slots != nullptr) {
-    // four slots a thread, of at most two pages
-    const int quads = (stride + 3) / 4;
-    for (long long q = gtid; q < (long long)units * quads; q += gsize) {
-      const int u = (int)(q / quads), i0 = (int)(q % quads) * 4;
+    // a warp takes 128 slots of a unit, a lane four of them (of at most two pages)
+    const int lane = tid & 31, per = (stride + 127) / 128;
+    const long long w0 = gtid / 32, nw = gsize / 32;
+    const int du = (int)(nw / per), dc = (int)(nw % per);
+    const bool wide = stride % 4 == 0 && (reinterpret_cast<uintptr_t>(slots) & 15) == 0;
+    int c = (int)(w0 % per);
+    for (long long u = w0 / per; u < units; u += du) {
       const int b = begin ? begin[u] : 0, r = rows[u], h = held[u];
       const UnitPages p = ok ? unit_pages(r, h, max_pages) : UnitPages{h, h};
       const int np = min(p.want, max_pages);           // pages that the unit has afterwards
+      const int i0 = c * 128 + lane * 4;
       auto page = [&](int j) -> int {
         if (j >= np) return -1;
-        if (j < p.held) return entry(u, j);
+        if (j < p.held) return entry((int)u, j);
         const int at = top + pre[u].x + j - p.held;
         return at < avail ? free_pages[at] : given_at(at - avail);
       };
@@ -173,21 +177,26 @@ page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* tab
         const long long t = (long long)b + i0 + k;
         out[k] = -1;
         if (b >= 0 && t < r) {
-          const int j = (int)(t / kPageRows);
+          const int j = (int)((unsigned)t / kPageRows);
           if (j != j_of) {
             j_of = j;
             id = page(j);
           }
-          if (id >= 0) out[k] = id * kPageRows + (int)(t % kPageRows);
+          if (id >= 0) out[k] = id * kPageRows + (int)((unsigned)t % kPageRows);
         }
       }
       int32_t* o = slots + (size_t)u * stride + i0;
-      if (stride % 4 == 0 && (reinterpret_cast<uintptr_t>(slots) & 15) == 0) {
+      if (wide && i0 < stride) {
         *reinterpret_cast<int4*>(o) = make_int4(out[0], out[1], out[2], out[3]);
       } else {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           if (i0 + k < stride) o[k] = out[k];
+      }
+      c += dc;
+      if (c >= per) {
+        c -= per;
+        ++u;
       }
     }
   }
@@ -224,12 +233,12 @@ cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32
   int2* pre = reinterpret_cast<int2*>(ws + Ly.pre);
   longlong2* total = reinterpret_cast<longlong2*>(ws + Ly.sums);
   int32_t* flags = reinterpret_cast<int32_t*>(ws);
-  // one CTA for what a CTA does in a few steps, else enough for four slots (or eight page
-  // numbers, if every page moved) a thread, up to one CTA per SM
+  // enough CTAs for four slots (or eight page numbers, if every page moved) a thread, up to four
+  // per SM (148 of 512 threads take 15.3 us where 592 of 256 take 13.9, 592 of 512 17.7)
   const long long work = (long long)units * stride / 4 > (long long)units * pool.max_pages / 8
                              ? (long long)units * stride / 4 : (long long)units * pool.max_pages / 8;
   long long ctas = (work + kAssignThreads - 1) / kAssignThreads;
-  if (ctas > kTargetCtas / 2) ctas = kTargetCtas / 2;
+  if (ctas > 2 * kTargetCtas) ctas = 2 * kTargetCtas;
   if (ctas < 1) ctas = 1;
   const bool local = units <= kAssignLocal;
   if (!local) {
@@ -252,10 +261,10 @@ cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32
 // channels after another. Codes of consecutive slots are then whole 128-byte lines (8 rows of 16
 // bytes; 4 pairs of 32), the maximum of a block is two shuffles away, and a lane has all the
 // loads of its row (8 of 16 bytes at d = 128 in bf16) in flight together. 262144 rows of d = 128 in
-// bf16 (175 MB of rows and pages): stored in 33.2 us, 5.3 TB/s = 0.81 of the measured copy peak, and
-// loaded in 30 us, 0.89. The store is near its issue rate too (79% of the slots): with two rows a
-// warp step and the codes masked and shifted into place one by one it took 61 us, the load 37.
-constexpr int kRowThreads = 256;
+// bf16 (175 MB of rows and pages): stored in 30.3 us, 5.8 TB/s = 0.88 of the measured copy peak, and
+// loaded in 29.1 us, 0.92. With two rows a warp step and the codes masked and shifted into place
+// one by one the store took 61 us, the load 37; blocks of 256 threads take 0.7 us longer.
+constexpr int kRowThreads = 128;
 constexpr int kRowsPerWarp = 8;
 constexpr int kRowsPerBlock = kRowThreads / 32 * kRowsPerWarp;
 
@@ -267,7 +276,7 @@ __device__ __forceinline__ bool paired(int slot, int lane) {
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 8)      // (left alone, the loads take turns in 40 registers)
 page_store_kernel(const T* __restrict__ K, const T* __restrict__ V, const float* __restrict__ logn,
                   const int32_t* __restrict__ slots, long long n_rows,
                   unsigned char* __restrict__ pages, int n_slots, int32_t* flags) {
@@ -330,7 +339,7 @@ page_store_kernel(const T* __restrict__ K, const T* __restrict__ V, const float*
 }
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kRowThreads)
+__global__ void __launch_bounds__(kRowThreads, 12)
 page_load_kernel(const unsigned char* __restrict__ pages, int n_slots,
                  const int32_t* __restrict__ slots, long long n_rows, T* __restrict__ K,
                  T* __restrict__ V, float* __restrict__ logn, int32_t* flags) {

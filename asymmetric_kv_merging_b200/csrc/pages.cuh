@@ -47,20 +47,15 @@ struct PageLayout {
   __host__ __device__ static constexpr int logn(int r) { return kLn + r * 4; }
 };
 
-// Smallest half >= amax / 7, as bits; NaN when there is none. The nearest half of the product
-// with 1/7 is at most one step off; 7 h is exact in fp32 (3 + 11 bits), so the comparisons that
-// move it are too.
+// Smallest half >= amax / 7, as bits; NaN when there is none. A product and a conversion that both
+// round up give it or the one above it; 7 h is exact in fp32 (3 + 11 bits), so the comparison that
+// tells is too.
 __device__ __forceinline__ uint32_t scale_bits(float amax) {
-  if (!(amax <= 7.f * 65504.f)) return 0x7fffu;
-  uint32_t h = __half_as_ushort(__float2half_rn(amax * (1.f / 7.f)));
-  if (h > 0x7bffu) h = 0x7bffu;                      // rounded up to infinity: 65504 does
-  const float v = __half2float(__ushort_as_half((unsigned short)h));
-  if (7.f * v < amax) return h + 1;
-  if (h > 0) {
-    const float w = __half2float(__ushort_as_half((unsigned short)(h - 1)));
-    if (7.f * w >= amax) return h - 1;
-  }
-  return h;
+  constexpr float kSeventh = 0.14285715f;            // the next fp32 above 1/7
+  static_assert(7.0 * kSeventh > 1.0, "rounded up");
+  uint32_t h = __half_as_ushort(__float2half_ru(__fmul_ru(amax, kSeventh)));
+  if (7.f * __half2float(__ushort_as_half((unsigned short)(h - 1))) >= amax) h -= 1;   // (NaN for h = 0: no)
+  return h > 0x7bffu ? 0x7fffu : h;
 }
 
 // The 8 codes of x[0..7] as nibbles, low first, for the scale with bits `sb`.
@@ -75,7 +70,6 @@ __device__ __forceinline__ uint32_t scale_bits(float amax) {
 // border has 4 bits).
 template <typename T>
 __device__ __forceinline__ uint32_t quantise8(const float* x, uint32_t sb) {
-  if (sb == 0u || sb == 0x7fffu) return 0x88888888u;
   const float s = __half2float(__ushort_as_half((unsigned short)sb));
   uint32_t w = 0;
   if constexpr (sizeof(T) == 2) {
@@ -93,7 +87,7 @@ __device__ __forceinline__ uint32_t quantise8(const float* x, uint32_t sb) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) w |= (uint32_t)(__float2int_rn(__fdiv_rn(x[i], s)) + 8) << (4 * i);
   }
-  return w;
+  return sb == 0u || sb == 0x7fffu ? 0x88888888u : w;      // nothing but zeros, or not representable
 }
 
 // 8 channels of a row as they are in the cache.

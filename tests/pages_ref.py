@@ -1,4 +1,4 @@
-"""The 4-bit paged cache in plain numpy and 64 bits: the checker of tests/test_gpu_pages.py.
+"""The 4-bit paged cache in plain numpy and 64 bits: the oracle of tests/test_gpu_pages.py.
 
 Shares no code with the library: format and page table rules are written out here from their
 definition in include/kvs.h, row by row.

@@ -1,4 +1,4 @@
-"""The 4-bit paged cache on the GPU against the plain 64-bit checker in tests/pages_ref.py.
+"""The 4-bit paged cache on the GPU against the plain 64-bit oracle in tests/pages_ref.py.
 
 Page tables, slot maps, page bytes and rows read back are exact. Decode outputs carry a bound
 that is derived, with A = sum_t p_t |v_t| and n rows:
@@ -321,7 +321,7 @@ class Cache:
         return worst
 
     def append(self, k_new, v_new, fits=None):
-        """The step's effect on the checker's pages and lengths; the device's must be the same."""
+        """The step's effect on the oracle's pages and lengths; the device's must be the same."""
         for u in range(self.B * self.H):
             if fits is None or fits[u]:
                 ref.put_row(self.pages_np, self.slot(u, int(self.lens_np[u])),
@@ -484,8 +484,8 @@ def test_decode_over_the_range_of_values(kvs, dtype, qs, ks, vs, ls, wide):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_decode_with_masked_rows(kvs, dtype, wide):
-    """Log-counts of -inf or of the type's lowest value take rows out; a unit of nothing but
-    -inf is zeros; the lowest value everywhere is a uniform shift."""
+    """Log-counts of -inf or near the type's lowest value take rows out; a unit of nothing but
+    -inf is zeros."""
     c = Cache(kvs, 1, 4, 4, 64, [70, 40, 65, 64], dtype, seed=9, wide=wide)
     low = float(np.finfo(np.float32).min)
     for u, t, x in [(0, t, -np.inf) for t in range(0, 70, 3)] + [(1, t, -np.inf) for t in range(40)] + \
@@ -530,7 +530,7 @@ def test_full_units_and_bad_pages(kvs, dtype, wide):
     c.table_np[0, 2:] = -1                                   # full: no page for row 64
     c.table_np[2, 1:] = -1
     c.table_np[4, 1] = len(c.pages_np)                       # past the pool: rows 32.. are skipped
-    c.lens_np[4] = 32                                        # what the checker sees of unit 4
+    c.lens_np[4] = 32                                        # what the oracle sees of unit 4
     c.to_device()
     c.lens[4] = 40
     q, kn, vn = c.random(1, 10, 64), c.random(1, 5, 64), c.random(1, 5, 64)

@@ -1,5 +1,5 @@
 """Host-side checks of the 4-bit paged cache's entry points (no GPU needed: nothing here
-launches), and of the checker the GPU tests use."""
+launches), and of the oracle the GPU tests use."""
 
 import ctypes
 
@@ -110,7 +110,7 @@ def test_decode_refusals(kvs):
     assert call(ws=None) == 4 and call(ws_bytes=4096) == 4
 
 
-def test_checker_rounds_to_nearest_even_and_bounds_the_error():
+def test_oracle_rounds_to_nearest_even_and_bounds_the_error():
     rng = np.random.default_rng(0)
     x = rng.standard_normal((200, 64)) * np.exp(rng.uniform(-12, 12, (200, 1)))
     code, s = ref.quantise(x)
@@ -127,7 +127,7 @@ def test_checker_rounds_to_nearest_even_and_bounds_the_error():
     assert np.isnan(ref.held(np.array([[np.inf] + [1.0] * 31]))).all()
 
 
-def test_checker_pages_round_trip():
+def test_oracle_pages_round_trip():
     rng = np.random.default_rng(1)
     for d in (64, 128):
         pages = np.zeros((2, ref.page_bytes(d)), np.uint8)
