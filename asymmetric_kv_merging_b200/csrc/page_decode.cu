@@ -87,7 +87,24 @@ struct PageClusterShape {
 // A lone full unit of 64 C pages among empty ones takes the cluster 12 us and the split kernel 9 to
 // 12; one of 128 C pages 18 us, a risk that is taken for the few units that C >= 8 means, as they are
 // mostly the heads of one sequence.
-static bool use_cluster(int C, int max_pages) { return C >= 2 && max_pages <= (C >= 8 ? 128 : 64) * C; }
+constexpr int kPcMaxPages = 128;                     // of a unit in one CTA
+static_assert(kPcMaxPages <= kPcWarps * 32, "a lane of the cluster kernel has one page at most");
+static bool use_cluster(int C, int clusters, int max_pages) {
+  return C >= 2 && max_pages <= (C >= 8 ? kPcMaxPages : kPcMaxPages / 2) * C * clusters;
+}
+
+// Clusters of a unit: one or two units with wide tables have 8 in all. A cluster has at most 16
+// CTAs, and 8 clusters of 10 run side by side. Measured (us, G = 4, d = 128; several clusters | what
+// it would be else): one unit with a table of 1025 pages 8.4 | 11.3 at 32768 rows, 7.4 | 5.7 at 2048;
+// with 4097 pages (else the split kernel) 12.4 | 26.0 at 131072 rows, 7.5 | 9.0 at 2048; two units of
+// 4097 pages 17.8 | 25.3 and 7.4 | 9.3. With 513 pages it is 7.9 | 8.2 when they are full and
+// 7.6 | 5.6 at 2048 rows, and four units of 1025 pages lose (12.5 | 11.7): the workspace's round
+// trip costs 1.6 us. The table's width decides, not a length: a unit's CTAs could read different
+// lengths once one of them has appended.
+constexpr int kPcWide = 1024;
+static int clusters_of(int units, int max_pages) {
+  return units <= 2 && max_pages > kPcWide ? 8 / units : 1;
+}
 
 // How many pages more than the mean the longest unit may have in a CTA for a split by units.
 // Measured (us, equal lengths; by units | even runs): 16 units x 8192 rows 12.5 | 15.4, 128 x 2048
@@ -1139,13 +1156,38 @@ page_decode_kernel(const PageArgs<T> a) {
   }
 }
 
+// Weighs the partials (m, l, A) of the 16 lanes of a half-warp and sums them up in every lane (A,
+// l); returns the reference.
+__device__ __forceinline__ float half_warp_sum(float4& A, float m, float& l) {
+  float M = m;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const float f = part_weight(m, l, M);
+  l *= f;
+  A.x *= f; A.y *= f; A.z *= f; A.w *= f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) {
+    l += __shfl_xor_sync(0xffffffffu, l, o);
+    A.x += __shfl_xor_sync(0xffffffffu, A.x, o);
+    A.y += __shfl_xor_sync(0xffffffffu, A.y, o);
+    A.z += __shfl_xor_sync(0xffffffffu, A.z, o);
+    A.w += __shfl_xor_sync(0xffffffffu, A.w, o);
+  }
+  return M;
+}
+
 // The same with one thread-block cluster per unit, for few units: the CTAs of the cluster take
 // the unit's pages in turn, and combine through distributed shared memory. The page numbers do
 // not depend on the other units' lengths, so they are loaded together with the length, and the
 // combine needs neither the workspace nor a round trip to it.
+//
+// One or two units with wide tables have several clusters each (gridDim.y = units x `clusters`,
+// clusters_of), which take the unit's pages in turn. Each CTA leaves its slice of its cluster's
+// output in the workspace, and of the CTAs with the same slice the last to arrive (a counter per
+// unit and slice; it is zero again then) joins them, in the clusters' order.
 template <typename T, int D, int G>
 __global__ void __launch_bounds__(kPcWarps * 32, 1)
-page_decode_cluster_kernel(const PageArgs<T> a) {
+page_decode_cluster_kernel(const PageArgs<T> a, int clusters) {
   using P = PageLayout<D>;
   using S = PageClusterShape<D, G>;
   constexpr int NW = kPcWarps, ST = kPcStages;
@@ -1160,14 +1202,16 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
   griddep_wait();                 // launched with programmatic stream serialisation
   griddep_launch_dependents();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int u = blockIdx.y, C = gridDim.x, rank = (int)cluster_ctarank();
+  const int C = gridDim.x, rank = (int)cluster_ctarank();
+  const int u = blockIdx.y / clusters, part = blockIdx.y % clusters;
   const int len = a.len[u], L = a.legal(len);
-  long long j = rank + (long long)C * (warp + NW * lane);      // this lane's page of list 0
-  int id = j < a.max_pages ? a.table[(size_t)u * a.max_pages + j] : -1;
+  const int first = part * C + rank, step = C * clusters;
+  const long long j = first + (long long)step * (warp + NW * lane);     // this lane's page
+  const int id = j < a.max_pages ? a.table[(size_t)u * a.max_pages + j] : -1;
   PageWarp<T, D, G> pw;
   pw.init(s_ones[warp], lane);
   pw.load(a.q + (size_t)u * G * D, lane);
-  if (L != len && rank == 0 && tid == 0) set_flag(a.flags, KVS_FLAG_BAD_LENGTH);
+  if (L != len && part == 0 && rank == 0 && tid == 0) set_flag(a.flags, KVS_FLAG_BAD_LENGTH);
   auto entry = [&]() -> uint32_t {
     const int n = (int)min((long long)kPageRows, L - j * kPageRows);
     if (n <= 0) return 0u;
@@ -1175,16 +1219,10 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
     set_flag(a.flags, KVS_FLAG_BAD_PAGE);
     return 0u;
   };
-  auto fill = [&]() -> uint32_t {
-    j += (long long)C * NW * 32;
-    if (j * kPageRows >= L) return 0u;
-    id = a.table[(size_t)u * a.max_pages + j];
-    return entry();
-  };
   PageRing<D, ST> pr;
   pr.start(a.pages, dsm + warp * ST * P::kBytes,
            reinterpret_cast<uint64_t*>(dsm + S::kRing + S::kAcc + S::kSum) + warp * ST, entry(), lane);
-  pr.next = fill();
+  pr.next = 0u;                   // (use_cluster: there is one list)
   // (every warp for itself: there is one unit, and a barrier would cost more)
   pw.prepare(lane);
   if constexpr (sizeof(T) == 4) {
@@ -1198,8 +1236,7 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
     const float sn = new_logit<T, D, G>(a, u, warp, lane);
     if (lane == 0) s_new[warp] = sn;
   }
-  const int np = pages_of(L);
-  if (!pr.run((np - rank + C * (NW - warp) - 1) / (C * NW), lane, fill,
+  if (!pr.run((pages_of(L) - first + step * (NW - warp) - 1) / (step * NW), lane, [] { return 0u; },
               [&](unsigned char* pg, int n) { pw.take(pg, n, lane); }))
     set_flag(a.flags, KVS_FLAG_TIMEOUT);
   pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
@@ -1229,27 +1266,50 @@ page_decode_cluster_kernel(const PageArgs<T> a) {
       m = ml.x;
       l = ml.y;
     }
-    float M = m;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float f = part_weight(m, l, M);
-    l *= f;
-    A.x *= f; A.y *= f; A.z *= f; A.w *= f;
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) {
-      l += __shfl_xor_sync(0xffffffffu, l, o);
-      A.x += __shfl_xor_sync(0xffffffffu, A.x, o);
-      A.y += __shfl_xor_sync(0xffffffffu, A.y, o);
-      A.z += __shfl_xor_sync(0xffffffffu, A.z, o);
-      A.w += __shfl_xor_sync(0xffffffffu, A.w, o);
+    const float M = half_warp_sum(A, m, l);
+    if (b < hi && src == 0) {
+      if (clusters == 1) {
+        finish_columns<T>(A, M, l, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
+                          a.out + (size_t)u * G * D + b * 4);
+      } else {
+        float* row = a.part + (((size_t)u * clusters + part) * NU + b) * 8;
+        *reinterpret_cast<float4*>(row) = A;
+        *reinterpret_cast<float2*>(row + 4) = make_float2(M, l);
+      }
     }
-    if (b < hi && src == 0)
-      finish_columns<T>(A, M, l, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
-                        a.out + (size_t)u * G * D + b * 4);
   }
   cluster_arrive();               // this CTA has read its peers; the wait is at the end
-  if (rank == 0 && a.k_new != nullptr) {
-    // every CTA of the cluster read the length before the first barrier
+  bool last = true;
+  if (clusters > 1) {
+    __shared__ int s_last;
+    __syncthreads();
+    if (tid == 0) s_last = atom_add_acq_rel_gpu(&a.counters[u * C + rank], 1) == clusters - 1;
+    __syncthreads();
+    last = s_last != 0;
+    if (last) {
+      for (int b0 = lo + 2 * warp; b0 < hi; b0 += 2 * NW) {
+        const int b = b0 + (lane >> 4), src = lane & 15;
+        const int g = min(b, NU - 1) * 4 / D, c = b * 4 % D;
+        float m = -INFINITY, l = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (b < hi && src < clusters) {
+          const float* row = a.part + (((size_t)u * clusters + src) * NU + b) * 8;
+          A = __ldcg(reinterpret_cast<const float4*>(row));
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(row + 4));
+          m = ml.x;
+          l = ml.y;
+        }
+        const float M = half_warp_sum(A, m, l);
+        if (b < hi && src == 0)
+          finish_columns<T>(A, M, l, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
+                            a.out + (size_t)u * G * D + b * 4);
+      }
+      if (tid == 0) a.counters[u * C + rank] = 0;
+    }
+  }
+  if (last && rank == 0 && a.k_new != nullptr) {
+    // every CTA read the length before its cluster's first barrier, and each cluster's first CTA
+    // has arrived by now
     if (new_id >= 0) {
       write_new_row<T, D>(a, u, len, new_id, warp, lane);
       if (tid == 0) a.len[u] = len + 1;
@@ -1266,11 +1326,11 @@ static bool allow_smem(const void* fn, size_t bytes) {
   return ensure_smem_attr(fn, bytes > 48 * 1024 ? bytes : 48 * 1024 + 16);
 }
 
-// Cluster size for a cluster per unit on the current device, or 0 when the split kernel is to be
-// used: the largest C <= 16 with C * units <= SM count for which the occupancy calculator places
-// all clusters at once. Cached per device and number of units.
+// Cluster size for `clusters` of them on the current device, or 0 when the split kernel is to be
+// used: the largest C <= 16 with C * clusters <= SM count for which the occupancy calculator places
+// all clusters at once. Cached per device and number of clusters.
 template <typename T, int D, int G>
-static int page_cluster_size(int units) {
+static int page_cluster_size(int clusters) {
   using S = PageClusterShape<D, G>;
   auto kfn = page_decode_cluster_kernel<T, D, G>;
   int dev = 0;
@@ -1278,18 +1338,18 @@ static int page_cluster_size(int units) {
   static std::mutex mu;
   static std::map<std::pair<int, int>, int> cache;
   std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(dev, units);
+  const auto key = std::make_pair(dev, clusters);
   const auto it = cache.find(key);
   if (it != cache.end()) return it->second;
   int sms = 0;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  int C = sms / units;
+  int C = sms / clusters;
   if (C > kMaxClusterSize) C = kMaxClusterSize;
   if (!allow_smem((const void*)kfn, S::kSmem)) C = 0;
   if (C > 8 && !ensure_nonportable_cluster((const void*)kfn)) C = 8;
   for (; C >= 2; --C) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C, units);
+    cfg.gridDim = dim3(C, clusters);
     cfg.blockDim = dim3(kPcWarps * 32);
     cfg.dynamicSmemBytes = S::kSmem;
     cudaLaunchAttribute at[1];
@@ -1300,7 +1360,7 @@ static int page_cluster_size(int units) {
     cfg.attrs = at;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, (const void*)kfn, &cfg) == cudaSuccess && n >= units) break;
+    if (cudaOccupancyMaxActiveClusters(&n, (const void*)kfn, &cfg) == cudaSuccess && n >= clusters) break;
   }
   (void)cudaGetLastError();   // a refused query leaves no error behind
   if (C < 2) C = 0;
@@ -1320,10 +1380,11 @@ static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_pa
                          reinterpret_cast<int32_t*>(ws + Ly.done),
                          reinterpret_cast<float*>(ws + Ly.part), reinterpret_cast<int32_t*>(ws)};
   count_launches(1);
-  const int C = page_cluster_size<T, D, G>(units);
-  if (use_cluster(C, pool.max_pages)) {
+  const int clusters = clusters_of(units, pool.max_pages);
+  const int C = page_cluster_size<T, D, G>(units * clusters);
+  if (use_cluster(C, clusters, pool.max_pages)) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C, units);
+    cfg.gridDim = dim3(C, units * clusters);
     cfg.blockDim = dim3(kPcWarps * 32);
     cfg.dynamicSmemBytes = PageClusterShape<D, G>::kSmem;
     cfg.stream = st;
@@ -1336,7 +1397,7 @@ static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_pa
     at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 2;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, page_decode_cluster_kernel<T, D, G>, a);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, page_decode_cluster_kernel<T, D, G>, a, clusters);
     return e != cudaSuccess ? e : cudaGetLastError();
   }
   auto kfn = page_decode_kernel<T, D, G>;

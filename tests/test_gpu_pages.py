@@ -252,7 +252,8 @@ def test_slots_past_the_pool_are_skipped(kvs):
 @pytest.fixture(params=[0, 5000], ids=["short-tables", "wide-tables"])
 def wide(request):
     """Columns added to the page tables: few units with short tables are decoded by a cluster of
-    CTAs each, long tables (and many units) by the kernel that splits the pages evenly."""
+    CTAs each (one or two units with longer tables by several), long tables (and many units) by the
+    kernel that splits the pages evenly."""
     return request.param
 
 
@@ -452,6 +453,64 @@ def long_cache(kvs, dtype, d, G, rows, n_pages, first, wide=0):
 def test_decode_of_very_long_units(kvs, dtype, d, G, rows, wide):
     n = -(-rows // PAGE)
     long_cache(kvs, dtype, d, G, rows, n + 5, 3, wide)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,G", [(64, 1), (64, 8), (128, 2), (128, 4)])
+@pytest.mark.parametrize("lens", [[0], [1], [9001], [4100, 33], [0, 2560], [31, 0]])
+def test_decode_of_one_or_two_units_with_wide_tables(kvs, dtype, d, G, lens):
+    """Several clusters a unit."""
+    c = Cache(kvs, 1, len(lens), G, d, lens, dtype, seed=20, room=3, logn_scale=3.0, wide=1100)
+    q = c.random(1, len(lens) * G, d, scale=2.0)
+    c.check(q, c.step(q))
+    assert c.lens.tolist() == lens and np.array_equal(c.pages.cpu().numpy(), c.pages_np)
+    for _ in range(3):
+        kn, vn = c.random(1, len(lens), d), c.random(1, len(lens), d)
+        first = c.step(q)
+        assert all(torch.equal(c.step(q), first) for _ in range(5))
+        c.check(q, c.step(q, kn, vn), kn, vn)
+        c.append(kn, vn)
+    assert kvs.device_flags(c.ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens", [[1500], [1500, 40]])
+def test_table_widths_take_turns_on_one_workspace(kvs, dtype, lens):
+    """The same pages through tables of every width, each with its own way to decode, one after
+    another: eager steps against the oracle, captured ones against them."""
+    def pools(c):
+        tables = [i32(np.concatenate([c.table_np, -np.ones((len(lens), n), np.int64)], 1))
+                  for n in (0, 1024 - c.table_np.shape[1], 1025 - c.table_np.shape[1], 30000)]
+        return [kvs.page_pool(c.pages, t) for t in tables]
+
+    eager, graph = (Cache(kvs, 1, len(lens), 4, 128, lens, dtype, seed=21, room=17) for _ in range(2))
+    q, kn, vn = eager.random(1, 4 * len(lens), 128), eager.random(1, len(lens), 128), eager.random(1, len(lens), 128)
+    lens0, pages0, at = graph.lens.clone(), graph.pages.clone(), pools(graph)
+    outs = [torch.empty_like(q) for _ in at]
+
+    def calls():
+        for pool, out in zip(at, outs):
+            kvs.page_decode_attn(graph.desc, q, pool, graph.lens, out, graph.ws, kn, vn)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        calls()
+    torch.cuda.current_stream().wait_stream(side)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        calls()
+    graph.lens.copy_(lens0)
+    graph.pages.copy_(pages0)
+    for _ in range(3):
+        g.replay()
+        for eager.pool, out in zip(pools(eager), outs):
+            want = eager.step(q, kn, vn)
+            eager.check(q, want, kn, vn)
+            eager.append(kn, vn)
+            assert torch.equal(out, want)
+        assert torch.equal(graph.lens, eager.lens) and torch.equal(graph.pages, eager.pages)
+    assert kvs.device_flags(eager.ws) == kvs.device_flags(graph.ws) == 0
 
 
 def test_pages_past_four_gigabytes(kvs):
