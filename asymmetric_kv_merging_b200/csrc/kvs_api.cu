@@ -399,6 +399,8 @@ kvs_status kvs_page_assign(const kvs_page_pool* pool, int32_t units, const int32
   if (s != KVS_OK) return s;
   if (units <= 0 || !rows || !held || !free_pages || !n_free || (slots && slot_stride <= 0))
     return KVS_ERR_INVALID_ARG;
+  constexpr int32_t kMost = INT32_MAX - 1024;          // (counted up to in steps of a block)
+  if (units > kMost || (slots && slot_stride > kMost)) return KVS_ERR_INVALID_ARG;
   if (!aligned(rows, 4) || !aligned(held, 4) || !aligned(free_pages, 4) || !aligned(n_free, 4) ||
       !aligned(slot_begin, 4) || !aligned(slots, 4))
     return KVS_ERR_INVALID_ARG;
@@ -418,7 +420,7 @@ kvs_status kvs_page_assign(const kvs_page_pool* pool, int32_t units, const int32
   s = check_ws(ws, ws_bytes, page_assign_ws(units).total);
   if (s != KVS_OK) return s;
   return from_cuda(launch_page_assign(*pool, units, rows, held, free_pages, n_free, slot_begin,
-                                      slots, slot_stride, static_cast<char*>(ws),
+                                      slots, slot_stride, static_cast<char*>(ws), ws_bytes,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -498,7 +500,7 @@ kvs_status kvs_page_decode_attn(const kvs_cache_desc* desc, const void* q,
   s = check_ws(ws, ws_bytes, page_layout_ws(*desc).total);
   if (s != KVS_OK) return s;
   return from_cuda(launch_page_decode(*desc, q, *pool, len, k_new, v_new, out,
-                                      static_cast<char*>(ws),
+                                      static_cast<char*>(ws), ws_bytes,
                                       reinterpret_cast<cudaStream_t>(stream)));
 }
 

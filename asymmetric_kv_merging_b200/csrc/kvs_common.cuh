@@ -236,7 +236,8 @@ inline DecodeLayout decode_layout(const kvs_cache_desc& d) {
 // The 4-bit paged cache. The decode's work split gives every CTA of one wave (two per SM) an
 // equal run of pages, so a CTA leaves at most two partial rows per query head: one of a unit
 // that began before it, one of a unit that goes on after it. `done` counts the CTAs that are
-// through with the lengths (inside the flag word's block).
+// through with the lengths (inside the flag word's block). The scratch (`part` bytes) lies at the
+// end of the workspace, so that calls with fewer units leave the counters of larger ones alone.
 constexpr int kPageDecodeCtas = kTargetCtas;
 struct PageLayoutWs {
   size_t done, counters, part, total;
@@ -245,17 +246,19 @@ struct PageLayoutWs {
 inline size_t page_persistent_bytes(int units) {
   return kWsAlign + align_up((size_t)units * sizeof(int32_t), kWsAlign);
 }
-// Scratch of the page table update: two offsets per unit and their sums after the persistent
-// region; its CTAs count themselves in the flag word's block, as the decode's do.
+// Where the last `bytes` (a multiple of kWsAlign) of a workspace begin.
+inline size_t ws_tail(size_t ws_bytes, size_t bytes) { return ws_bytes / kWsAlign * kWsAlign - bytes; }
+
+// Scratch of the page table update, at the end too: the sums of two counts and their offsets, two
+// per unit; its CTAs count themselves in the flag word's block, as the decode's do.
 struct PageAssignWs {
-  size_t done, pre, sums, total;
+  size_t done, scratch, total;
 };
 inline PageAssignWs page_assign_ws(int units) {
   PageAssignWs L;
   L.done = kWsAlign * 3 / 4;
-  L.pre = page_persistent_bytes(units);
-  L.sums = align_up(L.pre + (size_t)units * 2 * sizeof(int32_t), 16);
-  L.total = align_up(L.sums + 16, kWsAlign);
+  L.scratch = align_up(16 + (size_t)units * 2 * sizeof(int32_t), kWsAlign);
+  L.total = page_persistent_bytes(units) + L.scratch;
   return L;
 }
 
@@ -264,9 +267,8 @@ inline PageLayoutWs page_layout_ws(const kvs_cache_desc& d) {
   const int units = d.B * d.H_kv;
   L.done = kWsAlign / 2;
   L.counters = kWsAlign;
-  L.part = page_persistent_bytes(units);
-  const size_t part = (size_t)kPageDecodeCtas * 2 * (d.H_q / d.H_kv) * (d.d + kPartPad) * sizeof(float);
-  L.total = align_up(L.part + part, kWsAlign);
+  L.part = align_up((size_t)kPageDecodeCtas * 2 * (d.H_q / d.H_kv) * (d.d + kPartPad) * sizeof(float), kWsAlign);
+  L.total = page_persistent_bytes(units) + L.part;
   if (L.total < page_assign_ws(units).total) L.total = page_assign_ws(units).total;
   return L;
 }

@@ -78,7 +78,7 @@ cudaError_t launch_decode_tc(const kvs_cache_desc& d, const void* q, void* K, vo
 cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32_t* rows,
                                int32_t* held, int32_t* free_pages, int32_t* n_free,
                                const int32_t* begin, int32_t* slots, int stride, char* ws,
-                               cudaStream_t st);
+                               size_t ws_bytes, cudaStream_t st);
 cudaError_t launch_page_store(const kvs_cache_desc& d, const void* K, const void* V,
                               const float* logn, const int32_t* slots, const kvs_page_pool& pool,
                               char* ws, cudaStream_t st);
@@ -87,7 +87,7 @@ cudaError_t launch_page_load(const kvs_cache_desc& d, const kvs_page_pool& pool,
                              cudaStream_t st);
 cudaError_t launch_page_decode(const kvs_cache_desc& d, const void* q, const kvs_page_pool& pool,
                                int32_t* len, const void* k_new, const void* v_new, void* out,
-                               char* ws, cudaStream_t st);
+                               char* ws, size_t ws_bytes, cudaStream_t st);
 
 // Measurement helper: stream `rows` rows of a [rows, d] bf16 array through shared
 // memory with the decode kernel's TMA pattern on `ctas` CTAs, computing nothing.

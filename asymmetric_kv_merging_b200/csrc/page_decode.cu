@@ -24,9 +24,7 @@
 //   split    64 units x 11K..22K     38.3 us, 4.1 TB/s = 0.62 of the measured copy peak
 //           128 units x 1K..8K       29.0 us, 3.0 TB/s
 // The same kernels without the arithmetic take 4.1, 5.7, 10.2, 31.5 and 23.1 us.
-#include <map>
-#include <mutex>
-#include <utility>
+#include <atomic>
 
 #include "decode_common.cuh"
 #include "kvs_common.cuh"
@@ -61,7 +59,7 @@ struct PageDecodeShape {
 };
 
 // Weight of a partial (m, l, acc) against the reference M. One without a row that counts has
-// l = 0; NaN logits leave m at -inf and l NaN, which has to go through.
+// l = 0; where logits are NaN l is, which has to go through.
 __device__ __forceinline__ float part_weight(float m, float l, float M) {
   return l != 0.f ? ex2_ftz(m - M) : 0.f;
 }
@@ -123,8 +121,9 @@ __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast
 
 // One warp's share of a unit: its softmax state over the pages it has taken. load() and prepare()
 // make the unit's operands from its queries (share() and fetch() hand them from one warp to the
-// others), reset() starts a unit, take() adds the first nval rows of a page, end() writes the partial output
-// [G][D] and (m, l) per query head (log2 domain; m is a reference, not always the maximum).
+// others), reset() starts a unit, take() adds the first nval rows of a page, end() writes the
+// partial output [G][D] and (m, l) per query head (log2 domain; m is a reference, not always the
+// maximum, and -inf where no row counts).
 
 // fp32: CUDA cores, every product and sum in fp32 (two at a time where they come in pairs), so
 // that it stays within an fp32 softmax attention's own error. Logits with a lane per row, values
@@ -277,10 +276,6 @@ struct PageWarp {
 // unpacked register to tensor memory first. Fragments by ldmatrix instead of 27 more loads, the
 // reference inside the sums and the weight sums by MMA took the page from 507 to 450.
 
-// The reference before the first row: below every logit, and finite, so that masked rows (-inf)
-// have a weight of 0 against it.
-constexpr float kNoRef = -1e30f;
-
 template <int D, int G>
 struct PageWarp<bf16, D, G> {
   using P = PageLayout<D>;
@@ -289,8 +284,7 @@ struct PageWarp<bf16, D, G> {
   uint32_t qb[2 * NB][2];      // B of S^T: [2 b + i], k slots (8 t + 2 i, + 4) and (8 t + 2 i + 1, + 5)
   uint32_t cb[2];              // B of the offset: -8 2^-24 sum q' of the blocks, in three half parts
   float f0, f1;                // logit (log2) per unit of the scaled accumulators
-  float m0, m1;                // the references (log2), and as the start of a logit's sums:
-  float r0, r1;                // -m / f (0 while there is none)
+  float m0, m1;                // the references (log2; 0 while there is none)
   float lim0, lim1;            // a logit over the reference by more than this moves it
   float O[NB][2][4];           // sums of u w, of channels 4 g (+ 2) and of 4 g + 1 (+ 3) times 16 plus it
   float off[4];                // row b: sum_t p scale of block b; row 4: sum_t p
@@ -395,8 +389,7 @@ struct PageWarp<bf16, D, G> {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) O[b][0][i] = O[b][1][i] = 0.f;
-    m0 = m1 = kNoRef;
-    r0 = r1 = 0.f;
+    m0 = m1 = 0.f;
     lim0 = lim1 = -INFINITY;
     off[0] = off[1] = off[2] = off[3] = 0.f;
     poison = 0u;
@@ -435,7 +428,7 @@ struct PageWarp<bf16, D, G> {
       }
       const uint32_t za = as_u32(t & 1 ? sa[i][NB / 2 - 1] : sa[i][0]);
       const uint32_t zb = as_u32(t & 1 ? sb[i][NB / 2 - 1] : sb[i][0]);
-      mma_f16_16816_from(x[i], za, zb, za, zb, cb[0], cb[1], r0, r1);
+      mma_f16_16816_zero(x[i], za, zb, za, zb, cb[0], cb[1]);
     }
     const uint32_t base = smem_u32(pg);
 #pragma unroll
@@ -464,13 +457,16 @@ struct PageWarp<bf16, D, G> {
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      // Log-counts may be far from zero (-1e9 for a mask, say): logits are lost against one, but
+      // not against its difference to a reference near it. (The products stay rounded; fused into
+      // the differences they would not match the reference that came from them.)
       const int r = i * 16 + g;
-      const float na = *reinterpret_cast<const float*>(pg + P::logn(r)) * kLog2e;
-      const float nb = *reinterpret_cast<const float*>(pg + P::logn(r + 8)) * kLog2e;
-      x[i][0] = fmaf(x[i][0], f0, na);
-      x[i][1] = fmaf(x[i][1], f1, na);
-      x[i][2] = fmaf(x[i][2], f0, nb);
-      x[i][3] = fmaf(x[i][3], f1, nb);
+      const float na = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e);
+      const float nb = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r + 8)), kLog2e);
+      x[i][0] = fmaf(x[i][0], f0, na - m0);
+      x[i][1] = fmaf(x[i][1], f1, na - m1);
+      x[i][2] = fmaf(x[i][2], f0, nb - m0);
+      x[i][3] = fmaf(x[i][3], f1, nb - m1);
     }
     // The reference of a column moves only when a weight would pass 2^15, to where the largest is
     // 2^7: after the first pages that is rare. Scales above 1 take the same path, since p scale
@@ -486,11 +482,14 @@ struct PageWarp<bf16, D, G> {
     const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
     const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
     if (__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > lim0 || h1 > lim1)) {
-      float2 up = move_reference(pg, h0, h1, lane);
+      const float3 up = move_reference(pg, h0, h1, lane);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[i][0] -= up.x; x[i][1] -= up.y; x[i][2] -= up.x; x[i][3] -= up.y;
-      }
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float y = x[i][j] - (j & 1 ? up.y : up.x);
+          x[i][j] = y > up.z ? up.z : y;             // (a NaN stays)
+        }
     }
     __half2 pb[2][2];
 #pragma unroll
@@ -528,8 +527,10 @@ struct PageWarp<bf16, D, G> {
   }
 
   // The references for a page whose largest logits over them in this lane's columns and rows are
-  // h0, h1 (returns by how much they moved), and its blocks that read as NaN.
-  __device__ __forceinline__ float2 move_reference(unsigned char* pg, float h0, float h1, int lane) {
+  // h0, h1, and its blocks that read as NaN. Returns by how much the references moved, which is
+  // nothing where a move is lost against a reference far from zero, and what a logit may be at
+  // most, which matters only then.
+  __device__ __forceinline__ float3 move_reference(unsigned char* pg, float h0, float h1, int lane) {
     uint32_t smax = 0, nan = 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -553,8 +554,9 @@ struct PageWarp<bf16, D, G> {
       h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));
       h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
     }
-    const float u0 = h0 + ev > lim0 ? h0 + (ev - 7.f) : 0.f;
-    const float u1 = h1 + ev > lim1 ? h1 + (ev - 7.f) : 0.f;
+    const float n0 = h0 + ev > lim0 ? m0 + (h0 + (ev - 7.f)) : m0;
+    const float n1 = h1 + ev > lim1 ? m1 + (h1 + (ev - 7.f)) : m1;
+    const float u0 = n0 - m0, u1 = n1 - m1;
     // (before there is a reference, O and off are 0 and u may be anything)
     const float e0 = lim0 < 0.f ? 0.f : ex2_ftz(-u0), e1 = lim1 < 0.f ? 0.f : ex2_ftz(-u1);
 #pragma unroll
@@ -565,16 +567,14 @@ struct PageWarp<bf16, D, G> {
       }
     off[0] *= e0; off[1] *= e1; off[2] *= e0; off[3] *= e1;
     if (h0 > -INFINITY) {                            // (the column has a row that counts)
-      m0 = lim0 < 0.f ? u0 : m0 + u0;
-      r0 = -m0 / f0;
+      m0 = n0;
       lim0 = 15.f;
     }
     if (h1 > -INFINITY) {
-      m1 = lim1 < 0.f ? u1 : m1 + u1;
-      r1 = -m1 / f1;
+      m1 = n1;
       lim1 = 15.f;
     }
-    return make_float2(u0, u1);
+    return make_float3(u0, u1, 15.f - ev);
   }
 
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
@@ -598,11 +598,11 @@ struct PageWarp<bf16, D, G> {
     }
     if (g == 0) {
       if (2 * t < G) {
-        sm[2 * t] = m0;
+        sm[2 * t] = l0 != 0.f ? m0 : -INFINITY;
         sl[2 * t] = l0;
       }
       if (2 * t + 1 < G) {
-        sm[2 * t + 1] = m1;
+        sm[2 * t + 1] = l1 != 0.f ? m1 : -INFINITY;
         sl[2 * t + 1] = l1;
       }
     }
@@ -1332,15 +1332,12 @@ static bool allow_smem(const void* fn, size_t bytes) {
 template <typename T, int D, int G>
 static int page_cluster_size(int clusters) {
   using S = PageClusterShape<D, G>;
+  constexpr int kDevices = 64, kMost = 74;             // (148 SMs: no more clusters of two CTAs fit)
   auto kfn = page_decode_cluster_kernel<T, D, G>;
+  static std::atomic<signed char> cache[kDevices][kMost + 1];     // the size + 1, 0: not known
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-  static std::mutex mu;
-  static std::map<std::pair<int, int>, int> cache;
-  std::lock_guard<std::mutex> lock(mu);
-  const auto key = std::make_pair(dev, clusters);
-  const auto it = cache.find(key);
-  if (it != cache.end()) return it->second;
+  if (clusters > kMost || cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return 0;
+  if (const int known = cache[dev][clusters].load(std::memory_order_relaxed)) return known - 1;
   int sms = 0;
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   int C = sms / clusters;
@@ -1364,21 +1361,21 @@ static int page_cluster_size(int clusters) {
   }
   (void)cudaGetLastError();   // a refused query leaves no error behind
   if (C < 2) C = 0;
-  cache[key] = C;
+  cache[dev][clusters].store((signed char)(C + 1), std::memory_order_relaxed);
   return C;
 }
 
 template <typename T, int D, int G>
 static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_page_pool& pool,
                             int32_t* len, const void* k_new, const void* v_new, void* out,
-                            char* ws, cudaStream_t st) {
+                            char* ws, size_t ws_bytes, cudaStream_t st) {
   const int units = d.B * d.H_kv;
   const PageLayoutWs Ly = page_layout_ws(d);
   const PageArgs<T> a = {(const T*)q, (unsigned char*)pool.pages, pool.table, pool.n_pages,
                          pool.max_pages, len, (const T*)k_new, (const T*)v_new, (T*)out, units,
                          reinterpret_cast<int32_t*>(ws + Ly.counters),
                          reinterpret_cast<int32_t*>(ws + Ly.done),
-                         reinterpret_cast<float*>(ws + Ly.part), reinterpret_cast<int32_t*>(ws)};
+                         reinterpret_cast<float*>(ws + ws_tail(ws_bytes, Ly.part)), reinterpret_cast<int32_t*>(ws)};
   count_launches(1);
   const int clusters = clusters_of(units, pool.max_pages);
   const int C = page_cluster_size<T, D, G>(units * clusters);
@@ -1409,9 +1406,9 @@ static cudaError_t launch_t(const kvs_cache_desc& d, const void* q, const kvs_pa
 
 cudaError_t launch_page_decode(const kvs_cache_desc& d, const void* q, const kvs_page_pool& pool,
                                int32_t* len, const void* k_new, const void* v_new, void* out,
-                               char* ws, cudaStream_t st) {
+                               char* ws, size_t ws_bytes, cudaStream_t st) {
   const int G = d.H_q / d.H_kv;
-#define KVS_PD(TT, DD, GG) return launch_t<TT, DD, GG>(d, q, pool, len, k_new, v_new, out, ws, st)
+#define KVS_PD(TT, DD, GG) return launch_t<TT, DD, GG>(d, q, pool, len, k_new, v_new, out, ws, ws_bytes, st)
 #define KVS_PD_G(TT, DD)        \
   if (G == 1) KVS_PD(TT, DD, 1); \
   if (G == 2) KVS_PD(TT, DD, 2); \

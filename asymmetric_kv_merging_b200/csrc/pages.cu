@@ -228,10 +228,10 @@ page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* tab
 cudaError_t launch_page_assign(const kvs_page_pool& pool, int units, const int32_t* rows,
                                int32_t* held, int32_t* free_pages, int32_t* n_free,
                                const int32_t* begin, int32_t* slots, int stride, char* ws,
-                               cudaStream_t st) {
+                               size_t ws_bytes, cudaStream_t st) {
   const PageAssignWs Ly = page_assign_ws(units);
-  int2* pre = reinterpret_cast<int2*>(ws + Ly.pre);
-  longlong2* total = reinterpret_cast<longlong2*>(ws + Ly.sums);
+  longlong2* total = reinterpret_cast<longlong2*>(ws + ws_tail(ws_bytes, Ly.scratch));
+  int2* pre = reinterpret_cast<int2*>(total + 1);
   int32_t* flags = reinterpret_cast<int32_t*>(ws);
   // enough CTAs for four slots (or eight page numbers, if every page moved) a thread, up to four
   // per SM (148 of 512 threads take 15.3 us where 592 of 256 take 13.9, 592 of 512 17.7)

@@ -377,6 +377,7 @@ size_t kvs_page_bytes(int32_t d);
  * In/out: held [units] pages per unit (0 and table -1 at first), free_pages [n_pages],
  *      n_free (one int32): the stack of free page numbers, free_pages[0 .. *n_free).
  * Out: slots [units][slot_stride] (nullable).
+ * units and slot_stride below 2^31 - 1024.
  * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes with B * H_kv >= units.
  */
 kvs_status kvs_page_assign(const kvs_page_pool* pool, int32_t units, const int32_t* rows,
@@ -416,19 +417,22 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * page for that row sets KVS_FLAG_OUT_CAPACITY and is not changed (its output is written,
  * without the new row): reserve the row with kvs_page_assign first. A unit with nothing to
  * attend gets zeros. Rows whose page number is outside the pool are skipped
- * (KVS_FLAG_BAD_PAGE). T_cap of desc is not used (any valid value). Two units may share a page that neither
- * appends to.
+ * (KVS_FLAG_BAD_PAGE). A log-count of -inf, or one below -2.3e38 (its product with log2 e is
+ * -inf), leaves its row out. T_cap of desc is not used (any valid value). Two units may share a
+ * page that neither appends to.
  * Rounding: fp32 descriptors compute in fp32 throughout; with bf16 the softmax weights are
  * rounded to half precision (2^-11), alone and times a row's scale.
  * In:  q [B,H_q,d]; pool; len [B*H_kv], 0 <= len <= 32 max_pages;
  *      B * H_kv * (max_pages + 64) < 2^31.
  * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
  * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes; its counters must be zero at
- * the first call (each call leaves them zero). Make the first call for a device outside any
- * stream capture (it sets kernel attributes and asks the occupancy calculator). Few units
- * with short tables are decoded by a cluster of CTAs each, other calls by CTAs that split all
- * pages among them; the same call gives the same bits. Launched with programmatic stream
- * serialisation, in plain stream order, as kvs_decode_attn is.
+ * the first call (each call leaves them zero). One that is sized for the largest B serves
+ * every smaller one too (same heads and d), in any order. Make the first call for a device
+ * outside any stream capture (it sets kernel attributes and asks the occupancy calculator).
+ * Few units with short tables are decoded by a cluster of CTAs each, one or two with long
+ * ones by several, other calls by CTAs that split all pages among them; the same call gives
+ * the same bits. Launched with programmatic stream serialisation, in plain stream order, as
+ * kvs_decode_attn is.
  */
 kvs_status kvs_page_decode_attn(const kvs_cache_desc* desc, const void* q,
                                 const kvs_page_pool* pool, int32_t* len, const void* k_new,

@@ -52,7 +52,7 @@ def put_row(pages, slot, k, v, logn):
     """Quantise one row into pages [P, page_bytes] (uint8)."""
     d = len(k)
     pg = pages[slot // PAGE]
-    ko, vo, kso, vso, lo = _offsets(d, slot % PAGE)
+    ko, vo, kso, vso, _ = _offsets(d, slot % PAGE)
     for x, codes, scales in ((k, ko, kso), (v, vo, vso)):
         c, s = quantise(x)
         pg[codes] = c[0::2] | (c[1::2] << 4)
@@ -60,7 +60,13 @@ def put_row(pages, slot, k, v, logn):
         bits[np.isnan(s)] = 0x7fff
         for o, h in zip(scales, bits):
             pg[o], pg[o + 1] = h & 255, h >> 8
-    pg[lo:lo + 4] = np.frombuffer(np.float32(logn).tobytes(), np.uint8)
+    put_logn(pages, slot, logn)
+
+
+def put_logn(pages, slot, logn):
+    pg = pages[slot // PAGE]
+    at = len(pg) - 4 * PAGE + 4 * (slot % PAGE)
+    pg[at:at + 4] = np.frombuffer(np.float32(logn).tobytes(), np.uint8)
 
 
 def get_row(pages, slot, d):

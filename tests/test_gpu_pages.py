@@ -542,6 +542,46 @@ def test_decode_over_the_range_of_values(kvs, dtype, qs, ks, vs, ls, wide):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,lens", [(128, [3000, 33, 700]), (64, [31, 2049, 64]), (128, [300, 0, 200, 40] * 30)])
+@pytest.mark.parametrize("low", [-1e9, -1e30, -1e38, float(np.finfo(np.float32).min) / 2, 1e9])
+def test_log_counts_far_from_zero(kvs, dtype, d, lens, low, wide):
+    """Units whose rows all have the same one. Logits are within X (log2) of one another, so weights
+    relative to equal ones are within 2^(+-2 X), also where X is lost against the log-count; the
+    oracle's too: off by at most (2^(4 X) - 1) sum p |v|, and the roundings."""
+    c = Cache(kvs, 1, len(lens), 4, d, lens, dtype, seed=22, wide=wide)
+    for u, n in enumerate(lens):
+        for t in range(n):
+            ref.put_logn(c.pages_np, c.slot(u, t), low)
+    c.to_device()
+    q = c.random(1, 4 * len(lens), d, scale=2.0 ** -14)
+    got = c.step(q).double().cpu().numpy().reshape(len(lens), 4, d)
+    for u, n in enumerate(lens):
+        k, v, _ = ref.rows_of(c.pages_np, c.table_np[u], n, d)
+        qu = q.double().cpu().numpy().reshape(len(lens), 4, d)[u]
+        want, size = ref.attend(qu, k, v, np.zeros(n))
+        x = np.log2(np.e) * (np.abs(qu) @ np.abs(k).T).max(initial=0.0) / np.sqrt(d)
+        scales = ref.value_scales(c.pages_np, c.table_np[u], n, d)
+        bound = tolerance(dtype, qu, k, v, np.zeros(n), want, size, scales) + (2 ** (4 * x) - 1) * size
+        assert np.all(np.abs(got[u] - want) <= bound), (u, float((np.abs(got[u] - want) / bound).max()))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_log_counts_of_the_lowest_value_leave_rows_out(kvs, dtype, wide):
+    low = float(np.finfo(np.float32).min)
+    c = Cache(kvs, 1, 3, 4, 128, [100, 100, 100], dtype, seed=23, wide=wide)
+    for u, t in [(0, t) for t in range(100)] + [(1, t) for t in range(99)]:
+        ref.put_logn(c.pages_np, c.slot(u, t), low)
+    c.to_device()
+    q, kn, vn = c.random(1, 12, 128), c.random(1, 3, 128), c.random(1, 3, 128)
+    out = c.step(q)
+    assert not out[0, :4].any()
+    _, v, _ = ref.rows_of(c.pages_np, c.table_np[1], 100, 128)
+    assert np.allclose(out[0, 4:8].double().cpu().numpy(), v[99], rtol=2.0 ** -6, atol=1e-30)
+    out = c.step(q, kn, vn)                               # nothing but the new row
+    assert torch.equal(out[0, :4], vn[0, 0].expand(4, -1))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_decode_with_masked_rows(kvs, dtype, wide):
     """Log-counts of -inf or near the type's lowest value take rows out; a unit of nothing but
     -inf is zeros."""
@@ -648,6 +688,47 @@ def test_captured_steps_replay_like_eager_ones(kvs, wide):
         want = eager.step(q, kn, vn)
         assert torch.equal(out, want) and torch.equal(graph.lens, eager.lens)
         assert torch.equal(graph.pages, eager.pages)
+
+
+def test_one_workspace_for_batches_of_any_size(kvs):
+    """A workspace of the largest batch serves the smaller ones in between."""
+    big = Cache(kvs, 100, 1, 4, 128, [2500 if k % 10 == 9 else k % 40 for k in range(100)], torch.bfloat16,
+                seed=24)
+    small = Cache(kvs, 4, 5, 4, 128, [90 * k % 1100 for k in range(20)], torch.bfloat16, seed=25, wide=5000)
+    one = Cache(kvs, 1, 1, 4, 128, [3000], torch.bfloat16, seed=26, wide=1100)
+    qs = [c.random(c.B, 4 * c.H, 128) for c in (big, small, one)]
+    wants = [c.step(q) for c, q in zip((big, small, one), qs)]
+    small.ws = one.ws = big.ws
+    for _ in range(3):
+        for c, q, want in zip((small, big, one, big), [qs[i] for i in (1, 0, 2, 0)], [wants[i] for i in (1, 0, 2, 0)]):
+            assert torch.equal(c.step(q), want)
+    assert kvs.device_flags(big.ws) == 0
+
+
+def test_tables_of_fewer_units_than_the_workspace_has(kvs):
+    units, few, d = 6000, 4500, 64
+    g = torch.Generator(device=DEV).manual_seed(27)
+    pages = torch.randint(0, 256, (7 * units, kvs.page_bytes(d)), generator=g, device=DEV, dtype=torch.uint8)
+    pages[:, 32 * d:36 * d].view(torch.float16)[:] = 1.0
+    pages[:, 36 * d:] = 0
+    table = torch.arange(7 * units, dtype=torch.int32, device=DEV).view(units, 7)
+    pool = kvs.page_pool(pages, table)
+    desc = kvs.make_desc(1, units, units, d, 2, torch.bfloat16)
+    ws = kvs.workspace(desc, ops=(kvs.OP_PAGES,))
+    q = torch.randn(1, units, d, generator=g, device=DEV).to(torch.bfloat16)
+    lens, outs = torch.full((units,), 200, dtype=torch.int32, device=DEV), []
+    for _ in range(2):
+        out = torch.full_like(q, 99.0)
+        kvs.page_decode_attn(desc, q, pool, lens, out, ws)
+        outs.append(out)
+        table2 = torch.full((few, 2), -1, dtype=torch.int32, device=DEV)
+        held, free = torch.zeros(few, dtype=torch.int32, device=DEV), torch.arange(9000, dtype=torch.int32, device=DEV)
+        n_free = torch.tensor([9000], dtype=torch.int32, device=DEV)
+        rows = (torch.arange(few, device=DEV) % 60).to(torch.int32)
+        kvs.page_assign(kvs.page_pool(torch.zeros(9000, kvs.page_bytes(d), dtype=torch.uint8, device=DEV), table2),
+                        rows, held, free, n_free, ws)
+        assert torch.equal(held, (rows + 31) // 32)
+    assert torch.equal(*outs) and kvs.device_flags(ws) == 0
 
 
 def test_two_streams_with_a_workspace_each(kvs):
