@@ -13,17 +13,19 @@
 //    lies in one CTA is finished there; one that spans several gets a partial row per CTA in the
 //    workspace, and the last of them to arrive (a counter per unit) combines. No CTA waits for
 //    another.
-//  - cluster kernel: one thread-block cluster per unit, combined in distributed shared memory.
+//  - cluster kernel: one thread-block cluster per unit, combined in distributed shared memory (one
+//    or two units with wide tables: several, joined through the workspace).
 //
 // Measured on one B200 (G = 4, d = 128, bf16; device time of back-to-back launches over inputs
 // larger than L2; bytes are 148 a row):
 //   cluster   8 units x  2048 rows    6.2 us (2.4 MB: launch, three round trips and the combine)
-//             8 units x 16384 rows   10.9 us, 1.8 TB/s
+//             8 units x 16384 rows   11.0 us, 1.8 TB/s
 //             8 units x 32768 rows   16.6 us, 2.3 TB/s (80 SMs: ten CTAs are the largest cluster
 //                                    of which eight fit the GPU at once)
-//   split    64 units x 11K..22K     38.3 us, 4.1 TB/s = 0.62 of the measured copy peak
-//           128 units x 1K..8K       29.0 us, 3.0 TB/s
-// The same kernels without the arithmetic take 4.1, 5.7, 10.2, 31.5 and 23.1 us.
+//             1 unit x 131072 rows   12.5 us (8 clusters), 1.6 TB/s
+//   split    64 units x 11K..22K     38.6 us, 4.0 TB/s = 0.61 of the measured copy peak
+//           128 units x 1K..8K       29.2 us, 3.0 TB/s
+// The same kernels without the arithmetic take 4.1, 5.7, 10.2 us for 8 units, 31.5 and 23.1 us.
 #include <atomic>
 
 #include "decode_common.cuh"
@@ -267,14 +269,15 @@ struct PageWarp {
 // p at 2^7 (over scales above 1) or more when it was set, so weights down to 2^-21 of the largest
 // stay normal halves, and below that the error is at most 2^-25 / 2^7 of it.
 //
-// What bounds it: 450 instructions a page (32 rows, d = 128), of which 211 on the integer pipe,
+// What bounds it: 456 instructions a page (32 rows, d = 128), of which 214 on the integer pipe,
 // which takes one every other cycle, and 36 MMAs of 8 cycles on the tensor pipe of the legacy
 // MMAs; the two hardly overlap. About 197 cycles a page and SM, from 12 warps an SM on (20 warps
 // at 96 registers gain nothing), where an SM's share of the copy peak brings a page in 203: both
 // bounds at once. Converting the codes to half instead costs 8 conversions and 8 products a word
 // where this takes 4 or 5 integer operations; unpacking for tcgen05 would have to write every
-// unpacked register to tensor memory first. Fragments by ldmatrix instead of 27 more loads, the
-// reference inside the sums and the weight sums by MMA took the page from 507 to 450.
+// unpacked register to tensor memory first. Fragments by ldmatrix instead of 27 more loads and the
+// weight sums by MMA took the page from 507 to 450; the reference taken off the log-counts put 6
+// back (it started the logits' sums, and was lost there when it was far from zero).
 
 template <int D, int G>
 struct PageWarp<bf16, D, G> {

@@ -421,7 +421,8 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * -inf), leaves its row out. T_cap of desc is not used (any valid value). Two units may share a
  * page that neither appends to.
  * Rounding: fp32 descriptors compute in fp32 throughout; with bf16 the softmax weights are
- * rounded to half precision (2^-11), alone and times a row's scale.
+ * rounded to half precision (2^-11), alone and times a row's scale, and queries are below
+ * 2^117 in magnitude (one above it makes its head's output NaN).
  * In:  q [B,H_q,d]; pool; len [B*H_kv], 0 <= len <= 32 max_pages;
  *      B * H_kv * (max_pages + 64) < 2^31.
  * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
