@@ -287,8 +287,11 @@ struct PageWarp<bf16, D, G> {
   uint32_t qb[2 * NB][2];      // B of S^T: [2 b + i], k slots (8 t + 2 i, + 4) and (8 t + 2 i + 1, + 5)
   uint32_t cb[2];              // B of the offset: -8 2^-24 sum q' of the blocks, in three half parts
   float f0, f1;                // logit (log2) per unit of the scaled accumulators
-  float m0, m1;                // the references (log2; 0 while there is none)
-  float lim0, lim1;            // a logit over the reference by more than this moves it
+  // The reference of a column (log2) is base - c f: a log-count that the warp's logits are taken
+  // relative to (0 unless log-counts are far from zero), and what the accumulators start from.
+  float base, c0, c1;
+  // a logit over the reference by more than this moves it: 15, -inf while there is none
+  float lim0, lim1;
   float O[NB][2][4];           // sums of u w, of channels 4 g (+ 2) and of 4 g + 1 (+ 3) times 16 plus it
   float off[4];                // row b: sum_t p scale of block b; row 4: sum_t p
   // where this lane's row of `za` in take() is: 1 and an offset in the page, or 0 and an address
@@ -392,31 +395,18 @@ struct PageWarp<bf16, D, G> {
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) O[b][0][i] = O[b][1][i] = 0.f;
-    m0 = m1 = 0.f;
+    base = c0 = c1 = 0.f;
     lim0 = lim1 = -INFINITY;
     off[0] = off[1] = off[2] = off[3] = 0.f;
     poison = 0u;
   }
 
-  __device__ __forceinline__ void take(unsigned char* pg, int nval, int lane) {
-    constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u, BOTH = LO | HI;
+  // Logits (log2) of a page's rows relative to the references: rows g, g + 8 of 16 i .., columns 2 t, 2 t + 1.
+  __device__ __forceinline__ void logits(const unsigned char* pg, int lane, float (&x)[2][4]) const {
+    constexpr uint32_t LO = 0x000f000fu, HI = 0x00f000f0u;
     const int g = lane >> 2, t = lane & 3;
-    if (nval < kPageRows) {
-      // the page's other rows may hold anything: a logit of 0 - inf, and a weight of 0 for a value of 0
-      if (lane >= nval) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, lane)) = 0;
-          *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane)) = 0;
-        }
-        *reinterpret_cast<float*>(pg + P::logn(lane)) = -INFINITY;
-      }
-      fence_proxy_async_smem();      // the stage's next copy comes after these stores
-      __syncwarp();
-    }
     // the two groups of 16 rows side by side: each step's MMAs are independent of one another
     __half2 sa[2][NB / 2], sb[2][NB / 2];        // K scales of rows r and r + 8
-    float x[2][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i * 16 + g;
@@ -431,13 +421,13 @@ struct PageWarp<bf16, D, G> {
       }
       const uint32_t za = as_u32(t & 1 ? sa[i][NB / 2 - 1] : sa[i][0]);
       const uint32_t zb = as_u32(t & 1 ? sb[i][NB / 2 - 1] : sb[i][0]);
-      mma_f16_16816_zero(x[i], za, zb, za, zb, cb[0], cb[1]);
+      mma_f16_16816_cols(x[i], za, zb, za, zb, cb[0], cb[1], c0, c1);
     }
-    const uint32_t base = smem_u32(pg);
+    const uint32_t at = smem_u32(pg);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       uint32_t wa[2], wb[2];                       // word t of rows g, g + 8, g + 16, g + 24
-      ldsm_x4(base + P::k_code(b, 0) + lane * 16, wa[0], wb[0], wa[1], wb[1]);
+      ldsm_x4(at + P::k_code(b, 0) + lane * 16, wa[0], wb[0], wa[1], wb[1]);
       float a[2][4];
 #pragma unroll
       for (int i = 0; i < 2; ++i)
@@ -461,38 +451,54 @@ struct PageWarp<bf16, D, G> {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       // Log-counts may be far from zero (-1e9 for a mask, say): logits are lost against one, but
-      // not against its difference to a reference near it. (The products stay rounded; fused into
-      // the differences they would not match the reference that came from them.)
+      // not against its difference to a base near it. (The products stay rounded; fused into the
+      // differences they would not match the base that came from them.)
       const int r = i * 16 + g;
-      const float na = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e);
-      const float nb = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r + 8)), kLog2e);
-      x[i][0] = fmaf(x[i][0], f0, na - m0);
-      x[i][1] = fmaf(x[i][1], f1, na - m1);
-      x[i][2] = fmaf(x[i][2], f0, nb - m0);
-      x[i][3] = fmaf(x[i][3], f1, nb - m1);
+      const float na = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e) - base;
+      const float nb = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r + 8)), kLog2e) - base;
+      x[i][0] = fmaf(x[i][0], f0, na);
+      x[i][1] = fmaf(x[i][1], f1, na);
+      x[i][2] = fmaf(x[i][2], f0, nb);
+      x[i][3] = fmaf(x[i][3], f1, nb);
     }
-    // The reference of a column moves only when a weight would pass 2^15, to where the largest is
-    // 2^7: after the first pages that is rare. Scales above 1 take the same path, since p scale
-    // has to stay below 2^15 too, and so do NaN scales (adding 0x43ff carries a half above 1.0
-    // into its sign bit).
-    uint32_t big;
-    if constexpr (NB == 4) {
-      const uint2 w = *reinterpret_cast<const uint2*>(pg + P::kVs + lane * 8);
-      big = (w.x + 0x43ff43ffu) | (w.y + 0x43ff43ffu);
-    } else {
-      big = *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4) + 0x43ff43ffu;
-    }
-    const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
-    const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
-    if (__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > lim0 || h1 > lim1)) {
-      const float3 up = move_reference(pg, h0, h1, lane);
+  }
+
+  __device__ __forceinline__ void take(unsigned char* pg, int nval, int lane) {
+    constexpr uint32_t LO = 0x000f000fu, BOTH = 0x00ff00ffu;
+    const int g = lane >> 2, t = lane & 3;
+    if (nval < kPageRows) {
+      // the page's other rows may hold anything: a logit of 0 - inf, and a weight of 0 for a value of 0
+      if (lane >= nval) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float y = x[i][j] - (j & 1 ? up.y : up.x);
-          x[i][j] = y > up.z ? up.z : y;             // (a NaN stays)
+        for (int b = 0; b < NB; ++b) {
+          *reinterpret_cast<uint16_t*>(pg + P::k_scale(b, lane)) = 0;
+          *reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane)) = 0;
         }
+        *reinterpret_cast<float*>(pg + P::logn(lane)) = -INFINITY;
+      }
+      fence_proxy_async_smem();      // the stage's next copy comes after these stores
+      __syncwarp();
+    }
+    float x[2][4];
+    for (bool again = false;; again = true) {
+      logits(pg, lane, x);
+      // The reference of a column moves only when a weight would pass 2^15, to where the largest is
+      // 2^7: after the first pages that is rare. Scales above 1 take the same path, since p scale
+      // has to stay below 2^15 too, and so do NaN scales (adding 0x43ff carries a half above 1.0
+      // into its sign bit).
+      uint32_t big;
+      if constexpr (NB == 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(pg + P::kVs + lane * 8);
+        big = (w.x + 0x43ff43ffu) | (w.y + 0x43ff43ffu);
+      } else {
+        big = *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4) + 0x43ff43ffu;
+      }
+      const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
+      const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
+      if (!again && !__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > lim0 || h1 > lim1)) break;
+      if (!again && move_base(pg, lane)) continue;         // the logits are made anew
+      move_reference(pg, x, h0, h1, lane);
+      break;
     }
     __half2 pb[2][2];
 #pragma unroll
@@ -507,11 +513,12 @@ struct PageWarp<bf16, D, G> {
     // V scales of row pairs t, t + 4, t + 8, t + 12 of every block: each matrix eight times the same
     // 16 bytes. As A (`za`): row b the scales of block b, row 4 ones, so that the sums of weights
     // come with the sums of scaled weights.
+    const uint32_t at = smem_u32(pg);
     uint32_t sv[NB][4], za[4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      ldsm_x4(base + P::v_scale(b, 0) + (lane >> 3) * 16, sv[b][0], sv[b][1], sv[b][2], sv[b][3]);
-    ldsm_x4(base * za_page + za_off, za[0], za[1], za[2], za[3]);
+      ldsm_x4(at + P::v_scale(b, 0) + (lane >> 3) * 16, sv[b][0], sv[b][1], sv[b][2], sv[b][3]);
+    ldsm_x4(at * za_page + za_off, za[0], za[1], za[2], za[3]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = i * 16 + 2 * t;
@@ -529,11 +536,44 @@ struct PageWarp<bf16, D, G> {
     }
   }
 
-  // The references for a page whose largest logits over them in this lane's columns and rows are
-  // h0, h1, and its blocks that read as NaN. Returns by how much the references moved, which is
-  // nothing where a move is lost against a reference far from zero, and what a logit may be at
-  // most, which matters only then.
-  __device__ __forceinline__ float3 move_reference(unsigned char* pg, float h0, float h1, int lane) {
+  // A log-count (log2) further than this above the base becomes the new base: its distance to the
+  // ones that matter then costs a logit 2^-14 at most.
+  static constexpr float kFar = 1024.f;
+
+  // Takes the base to the page's largest log-count if that is far above it, or if it is far below
+  // and no row has counted yet. The old reference, which the new logits would be lost against, is
+  // left in lim (relative to the new base, so far below 0) for move_reference to join with them.
+  __device__ __forceinline__ bool move_base(const unsigned char* pg, int lane) {
+    const float top = redux_max(__fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(lane)), kLog2e));
+    if (!(fabsf(top - base) > kFar)) return false;
+    if (fabsf(top) == INFINITY || (top < base && __any_sync(0xffffffffu, fmaxf(lim0, lim1) > 0.f))) return false;
+    const float r0 = (base - top) - c0 * f0, r1 = (base - top) - c1 * f1;
+    base = top;
+    // a reference that logits put so high that it is near the new base, or above it, stays
+    c0 = lim0 > 0.f && r0 > -kFar ? -r0 / f0 : 0.f;
+    c1 = lim1 > 0.f && r1 > -kFar ? -r1 / f1 : 0.f;
+    if (lim0 > 0.f && r0 <= -kFar) lim0 = r0;
+    if (lim1 > 0.f && r1 <= -kFar) lim1 = r1;
+    return true;
+  }
+
+  // How far the reference of a column moves for a page whose largest logit over it is h (2^ev > every
+  // V scale): up to where the largest weight is 2^7, if one would pass 2^15. lim < 0: there is
+  // none yet, or one left by move_base.
+  static __device__ __forceinline__ float move_of(float h, float ev, float lim) {
+    const float u = h + (ev - 7.f);
+    return lim < 0.f ? fmaxf(u, lim) : h + ev > lim ? u : 0.f;
+  }
+
+  static __device__ __forceinline__ float advance(float& c, float f, float u) {
+    const float dc = u > -INFINITY ? __fdividef(u, f) : 0.f;
+    c -= dc;
+    return dc * f;
+  }
+
+  // The references for a page whose logits over them are x, the largest in this lane's columns and
+  // rows h0, h1, and its blocks that read as NaN. x becomes relative to the new references.
+  __device__ __forceinline__ void move_reference(unsigned char* pg, float (&x)[2][4], float h0, float h1, int lane) {
     uint32_t smax = 0, nan = 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -557,11 +597,9 @@ struct PageWarp<bf16, D, G> {
       h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));
       h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
     }
-    const float n0 = h0 + ev > lim0 ? m0 + (h0 + (ev - 7.f)) : m0;
-    const float n1 = h1 + ev > lim1 ? m1 + (h1 + (ev - 7.f)) : m1;
-    const float u0 = n0 - m0, u1 = n1 - m1;
-    // (before there is a reference, O and off are 0 and u may be anything)
-    const float e0 = lim0 < 0.f ? 0.f : ex2_ftz(-u0), e1 = lim1 < 0.f ? 0.f : ex2_ftz(-u1);
+    // the moves as the accumulators will hold them (0 where no row counts in the column yet)
+    const float u0 = advance(c0, f0, move_of(h0, ev, lim0)), u1 = advance(c1, f1, move_of(h1, ev, lim1));
+    const float e0 = ex2_ftz((lim0 < 0.f ? lim0 : 0.f) - u0), e1 = ex2_ftz((lim1 < 0.f ? lim1 : 0.f) - u1);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -569,20 +607,36 @@ struct PageWarp<bf16, D, G> {
         O[b][j][0] *= e0; O[b][j][1] *= e1; O[b][j][2] *= e0; O[b][j][3] *= e1;
       }
     off[0] *= e0; off[1] *= e1; off[2] *= e0; off[3] *= e1;
-    if (h0 > -INFINITY) {                            // (the column has a row that counts)
-      m0 = n0;
-      lim0 = 15.f;
-    }
-    if (h1 > -INFINITY) {
-      m1 = n1;
-      lim1 = 15.f;
-    }
-    return make_float3(u0, u1, 15.f - ev);
+    if (fmaxf(h0, lim0) > -INFINITY) lim0 = 15.f;
+    if (fmaxf(h1, lim1) > -INFINITY) lim1 = 15.f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        // (a move far from 0 is rounded; a weight may not pass 2^15 for that)
+        const float y = x[i][j] - (j & 1 ? u1 : u0);
+        x[i][j] = y > 15.f - ev ? 15.f - ev : y;     // (a NaN stays)
+      }
   }
 
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
     const int g = lane >> 2, t = lane & 3;
     constexpr float kUp = 16777216.f;
+    const float r0 = -c0 * f0, r1 = -c1 * f1;        // the references are base + r
+    const float m0 = base + r0, m1 = base + r1;
+    if (base != 0.f) {
+      // what the sum's rounding has lost goes into the sums (up to 2^100, which only logits of
+      // more than 70 beside log-counts of more than 1e9 pass)
+      const float e0 = ex2_ftz(fminf(fmaxf((base - m0) + r0, -100.f), 100.f));
+      const float e1 = ex2_ftz(fminf(fmaxf((base - m1) + r1, -100.f), 100.f));
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          O[b][j][0] *= e0; O[b][j][1] *= e1; O[b][j][2] *= e0; O[b][j][3] *= e1;
+        }
+      off[0] *= e0; off[1] *= e1;
+    }
     const float l0 = __shfl_sync(0xffffffffu, off[0], 16 + t), l1 = __shfl_sync(0xffffffffu, off[1], 16 + t);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {

@@ -162,6 +162,15 @@ __device__ __forceinline__ void mma_f16_16816_zero(float (&d)[4], uint32_t a0, u
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// D = A * B + c, the columns 2 t and 2 t + 1 of a lane starting at c0 and c1.
+__device__ __forceinline__ void mma_f16_16816_cols(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                   uint32_t a2, uint32_t a3, uint32_t b0,
+                                                   uint32_t b1, float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%10,%11,%10,%11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 
 // Byte offset of 16-byte chunk `chunk` (0..7) of row `row` inside a box written by TMA
 // with 128-byte swizzling (rows of 128 bytes, box base 1024-byte aligned).
@@ -444,6 +453,13 @@ __device__ __forceinline__ float ex2_ftz(float x) {
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// Maximum over a warp (sm_100; NaN is ignored).
+__device__ __forceinline__ float redux_max(float a) {
+  float d;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(a));
   return d;
 }
 

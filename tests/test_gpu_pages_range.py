@@ -1,0 +1,167 @@
+"""The paged decode over long units whose log-counts or values lie far apart, against softmax
+attention in 64 bits.
+
+The rows go into the pages by kvs_page_store and come back by kvs_page_load in fp32, where both are
+exact (tests/test_gpu_pages.py), so the oracle sees what the pages hold. Everything is batched over
+the units on the device: these units are too long for the row-by-row oracle.
+
+Bounds, with A = sum_t p_t |v_t|, n rows, X = max |q k| / sqrt(d) plus the largest log-count that a
+row with a weight has:
+  both   2 (d + 6) 2^-24 X for the roundings of a logit, n + 16 roundings of the sums and 2^-21 for
+         the exponentials, relative to A;
+  bf16   2^-11 (A + |out|) for the weights, rounded to half; 15 2^-11 S, S = sum_t p_t s_t, for weight
+         times scale, whose error counts on a code u <= 15; below the half range both are off by half
+         a subnormal step, 2^-25, the largest weight being at least 2^7: n 2^-32 2 |v| for the
+         weights, and n 2^-32 15 U for their products with the scales, which a warp holds in units of
+         U >= 2^-k of its block: 1 while the largest scale of the block lies in (2^-6, 1], else the
+         power of two above that scale (so at most twice it); scales above 1 are brought down to
+         that unit and may leave the half range there: 7 2^-25 U; and 2^-8 |out| for the output.
+"""
+
+import gc
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda")
+PAGE = 32
+
+
+@pytest.fixture(scope="module")
+def kvs():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    from asymmetric_kv_merging_b200 import build
+    build.build()
+    from asymmetric_kv_merging_b200 import kvs as mod
+    yield mod
+    gc.collect()
+    torch.cuda.empty_cache()             # later tests watch the device's free memory
+
+
+class Units:
+    """`units` KV heads of T rows each (T even) in shuffled pages, made from fp32 rows."""
+
+    def __init__(self, kvs, units, T, G, d, dtype, seed, k_scale=1.0, v_scale=1.0, wide=0):
+        self.kvs, self.units, self.T, self.G, self.d, self.dtype = kvs, units, T, G, d, dtype
+        self.gen = torch.Generator(device=DEV).manual_seed(seed)
+        self.K = k_scale * self.randn(1, units, T, d)
+        self.V = v_scale * self.randn(1, units, T, d)
+        self.logn = torch.zeros(1, units, T, device=DEV)
+        self.wide = wide
+
+    def randn(self, *shape):
+        return torch.randn(*shape, generator=self.gen, device=DEV)
+
+    def store(self):
+        kvs, units, T = self.kvs, self.units, self.T
+        per = T // PAGE + 1                                   # room for one row more
+        self.pages = torch.full((units * per + 3, kvs.page_bytes(self.d)), 255, dtype=torch.uint8, device=DEV)
+        order = torch.randperm(units * per, generator=self.gen, device=DEV).to(torch.int32).view(units, per) + 3
+        self.table = torch.full((units, per + self.wide), -1, dtype=torch.int32, device=DEV)
+        self.table[:, :per] = order
+        self.pool = kvs.page_pool(self.pages, self.table)
+        t = torch.arange(T, device=DEV)
+        slots = (order[:, t // PAGE] * PAGE + t % PAGE).to(torch.int32).view(1, units, T)
+        f32 = kvs.make_desc(1, units, units, self.d, T, torch.float32)
+        self.desc = kvs.make_desc(1, units, units * self.G, self.d, 2, self.dtype)
+        self.ws = kvs.workspace(self.desc, ops=(kvs.OP_PAGES,))
+        kvs.page_store(f32, self.K, self.V, self.logn, slots, self.pool, self.ws)
+        kvs.page_load(f32, self.pool, slots, self.K, self.V, None, self.ws)
+        self.lens = torch.full((units,), T, dtype=torch.int32, device=DEV)
+        return self
+
+    def queries(self, scale):
+        return (scale * self.randn(1, self.units * self.G, self.d)).to(self.dtype)
+
+    def decode(self, q, k_new=None, v_new=None):
+        out = torch.full_like(q, 99.0)
+        self.kvs.page_decode_attn(self.desc, q, self.pool, self.lens, out, self.ws, k_new, v_new)
+        assert self.kvs.device_flags(self.ws) == 0
+        return out
+
+    def scales(self, u):
+        """The scales [T, d / 32] of a unit's values."""
+        at = self.table[u, :-(-self.T // PAGE)].long()
+        s = self.pages[at, 34 * self.d:36 * self.d].view(torch.float16).view(len(at), -1, PAGE)
+        return s.transpose(1, 2).reshape(-1, self.d // 32)[:self.T].double()
+
+    def check(self, q, out, extra=0.0):
+        """`extra`: what log-counts of rows without a weight add to X."""
+        d, T, worst = self.d, self.T, 0.0
+        q, out = (x.view(self.units, self.G, d).double() for x in (q, out))
+        for u in range(self.units):
+            k, v, ln = self.K[0, u].double(), self.V[0, u].double(), self.logn[0, u].double()
+            ln = ln - ln.max()                               # the same softmax, and exact
+            w = torch.softmax(q[u] @ k.T / d ** 0.5 + ln, -1)
+            want, size = w @ v, w @ v.abs()
+            live = w.amax(0) > 0
+            x = float((q[u].abs() @ k[live].abs().T).max()) / d ** 0.5 + float(ln[live].abs().max()) + extra
+            bound = (2 * (d + 6) * 2.0 ** -24 * x + (T + 16) * 2.0 ** -24 + 2.0 ** -21) * size
+            bound += 2.0 ** -24 * want.abs()
+            if self.dtype == torch.bfloat16:
+                s = self.scales(u).repeat_interleave(32, 1)
+                top = s.max(0).values
+                unit = torch.where((top > 2.0 ** -6) & (top <= 1), 1.0, 2 * top)
+                bound += 2.0 ** -11 * (size + want.abs()) + 15 * 2.0 ** -11 * (w @ s) + 2.0 ** -8 * want.abs()
+                bound += T * 2.0 ** -32 * (2 * v.abs().max(0).values + 15 * unit) + 7 * 2.0 ** -25 * unit
+            err = (out[u] - want).abs()
+            worst = max(worst, float((err / bound).max()))
+            assert bool((err <= bound).all()), (u, worst, float((err / want.abs().clamp(min=1e-30)).median()))
+        return worst
+
+
+@pytest.fixture(params=[(8, 0), (8, 5000), (2, 1100), (80, 0)], ids=["cluster", "split", "clusters", "many"])
+def shape(request):
+    """Units, and columns added to their page tables: each way that a call may be decoded."""
+    return request.param
+
+
+LOW = [-1e4, -1e6, -1e9, -1e30, -1e38]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", LOW)
+@pytest.mark.parametrize("masked", ["first half", "every other page", "all but the last page", "last half"])
+def test_rows_masked_by_a_large_negative_log_count(kvs, dtype, shape, low, masked):
+    """Pages of masked rows before, between and after pages of rows that count."""
+    units, wide = shape
+    T = 16384 + 64 if units * (1 + wide) == 8 else 4096 + 64         # (several pages a warp)
+    c = Units(kvs, units, T, 4, 128, dtype, seed=1, wide=wide)
+    t = torch.arange(T, device=DEV)
+    off = {"first half": t < T // 2, "every other page": t // PAGE % 2 == 0, "all but the last page": t < T - PAGE,
+           "last half": t >= T // 2}[masked]
+    c.logn[:] = torch.rand(units, T, generator=c.gen, device=DEV)
+    c.logn[:, :, off] = low
+    c.store()
+    q = c.queries(2.0)
+    c.check(q, c.decode(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_log_counts_that_climb(kvs, dtype, shape):
+    """Every page's log-counts above the last one's, by steps that the reference follows and by
+    steps that it would be lost against; rows of the last two pages count."""
+    units, wide = shape
+    T = 64 * PAGE
+    for step in (15.0, 600.0, 1000.0, 3e4, 1e7):
+        c = Units(kvs, units, T, 2, 64, dtype, seed=2, wide=wide)
+        page = torch.arange(T, device=DEV) // PAGE
+        c.logn[:] = torch.where(page >= 62, 0.0, (page - 62) * step)
+        c.store()
+        q = c.queries(2.0)
+        # what counts may be up to 1024 log 2 above the log-count that a warp's logits are relative to
+        c.check(q, c.decode(q), extra=720.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16])
+@pytest.mark.parametrize("low", LOW + [1e6, 1e9, 1e30])
+def test_logits_count_beside_a_far_log_count_that_all_rows_have(kvs, dtype, shape, low):
+    """Logits of tens: neither lost beside the log-count, nor cut off."""
+    units, wide = shape
+    c = Units(kvs, units, 4096, 4, 64, dtype, seed=3, wide=wide)
+    c.logn[:] = low
+    c.store()
+    q = c.queries(8.0)
+    c.check(q, c.decode(q))
