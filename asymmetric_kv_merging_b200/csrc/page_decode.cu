@@ -265,9 +265,11 @@ struct PageWarp {
 //      of the weights); it does not see the rounding of w, which therefore counts on |u| <= 15
 //      instead of |u - 8| <= 7. Of two channels in a byte one is summed alone and the other as
 //      u + 16 u'; the difference is taken at the end.
-// p and w are rounded to half (2^-11 each); the reference m keeps p scale <= 2^15 and the largest
-// p at 2^7 (over scales above 1) or more when it was set, so weights down to 2^-21 of the largest
-// stay normal halves, and below that the error is at most 2^-25 / 2^7 of it.
+// p and w are rounded to half (2^-11 each); the reference m keeps p <= 2^15 and the largest p at 2^7
+// or more when it was set, so weights down to 2^-21 of the largest stay normal halves, and below
+// that the error is at most 2^-25 / 2^7 of it. For w the same holds with the scales in units of
+// scale_values (with scales taken as they are, those of 2^-17 lost a third of their range, and
+// what a row lost of u w stayed in 8 scale p).
 //
 // What bounds it: 456 instructions a page (32 rows, d = 128), of which 214 on the integer pipe,
 // which takes one every other cycle, and 36 MMAs of 8 cycles on the tensor pipe of the legacy
@@ -296,7 +298,20 @@ struct PageWarp<bf16, D, G> {
   float off[4];                // row b: sum_t p scale of block b; row 4: sum_t p
   // where this lane's row of `za` in take() is: 1 and an offset in the page, or 0 and an address
   uint32_t za_page, za_off;
-  uint32_t poison;             // bit b: block b of some row reads as NaN
+  // V scales are taken times 2^k, k of each block's own (kNoUnit: no scale but 0 yet); see scale_values.
+  // k + 32 of block b from bit kAt(b) on; bit 12 (13, 28, 29): block 0 (1, 2, 3) of some row reads as
+  // NaN; bit 31: some k is not 0.
+  uint32_t units;
+  static constexpr int kNoUnit = 24;
+  static __host__ __device__ constexpr int kAt(int b) { return (b & 1) * 6 + (b >> 1) * 16; }
+  static __host__ __device__ constexpr uint32_t kNan(int b) { return 1u << (12 + (b & 1) + (b >> 1) * 16); }
+  static __host__ __device__ constexpr uint32_t kAll(int k) {
+    uint32_t u = k != 0 ? 1u << 31 : 0u;
+    for (int b = 0; b < NB; ++b) u |= (uint32_t)(k + 32) << kAt(b);
+    return u;
+  }
+  __device__ __forceinline__ int unit(int at) const { return (int)(units >> at & 63u) - 32; }
+  static __device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
   // `ones_`: 32 bytes of shared memory of this warp's own
   __device__ __forceinline__ void init(__half* ones_, int lane) {
@@ -398,7 +413,7 @@ struct PageWarp<bf16, D, G> {
     base = c0 = c1 = 0.f;
     lim0 = lim1 = -INFINITY;
     off[0] = off[1] = off[2] = off[3] = 0.f;
-    poison = 0u;
+    units = kAll(kNoUnit);
   }
 
   // Logits (log2) of a page's rows relative to the references: rows g, g + 8 of 16 i .., columns 2 t, 2 t + 1.
@@ -483,21 +498,24 @@ struct PageWarp<bf16, D, G> {
     for (bool again = false;; again = true) {
       logits(pg, lane, x);
       // The reference of a column moves only when a weight would pass 2^15, to where the largest is
-      // 2^7: after the first pages that is rare. Scales above 1 take the same path, since p scale
-      // has to stay below 2^15 too, and so do NaN scales (adding 0x43ff carries a half above 1.0
-      // into its sign bit).
-      uint32_t big;
+      // 2^7: after the first pages that is rare. Scales out of range are rare too: above 1 (adding
+      // 0x43ff carries a half above 1.0 into its sign bit; NaN as well), or, while a warp has met
+      // small ones only, all of them.
+      uint32_t odd = units;
       if constexpr (NB == 4) {
         const uint2 w = *reinterpret_cast<const uint2*>(pg + P::kVs + lane * 8);
-        big = (w.x + 0x43ff43ffu) | (w.y + 0x43ff43ffu);
+        odd |= (w.x + 0x43ff43ffu) | (w.y + 0x43ff43ffu);
       } else {
-        big = *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4) + 0x43ff43ffu;
+        odd |= *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4) + 0x43ff43ffu;
       }
       const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
       const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
-      if (!again && !__any_sync(0xffffffffu, (big & 0x80008000u) != 0u || h0 > lim0 || h1 > lim1)) break;
-      if (!again && move_base(pg, lane)) continue;         // the logits are made anew
-      move_reference(pg, x, h0, h1, lane);
+      const bool far = h0 > lim0 || h1 > lim1;
+      if (!again && !__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u || far)) break;
+      const bool move = again || __any_sync(0xffffffffu, far);
+      if (move && !again && move_base(pg, lane)) continue;       // the logits are made anew
+      if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u)) scale_values(pg, lane);
+      if (move) move_reference(x, h0, h1);
       break;
     }
     __half2 pb[2][2];
@@ -557,12 +575,11 @@ struct PageWarp<bf16, D, G> {
     return true;
   }
 
-  // How far the reference of a column moves for a page whose largest logit over it is h (2^ev > every
-  // V scale): up to where the largest weight is 2^7, if one would pass 2^15. lim < 0: there is
-  // none yet, or one left by move_base.
-  static __device__ __forceinline__ float move_of(float h, float ev, float lim) {
-    const float u = h + (ev - 7.f);
-    return lim < 0.f ? fmaxf(u, lim) : h + ev > lim ? u : 0.f;
+  // How far the reference of a column moves for a page whose largest logit over it is h: up to where
+  // the largest weight is 2^7, if one would pass 2^15. lim < 0: there is none yet, or one left by
+  // move_base.
+  static __device__ __forceinline__ float move_of(float h, float lim) {
+    return lim < 0.f ? fmaxf(h - 7.f, lim) : h > lim ? h - 7.f : 0.f;
   }
 
   static __device__ __forceinline__ float advance(float& c, float f, float u) {
@@ -571,34 +588,85 @@ struct PageWarp<bf16, D, G> {
     return dc * f;
   }
 
-  // The references for a page whose logits over them are x, the largest in this lane's columns and
-  // rows h0, h1, and its blocks that read as NaN. x becomes relative to the new references.
-  __device__ __forceinline__ void move_reference(unsigned char* pg, float (&x)[2][4], float h0, float h1, int lane) {
-    uint32_t smax = 0, nan = 0;
+  // Brings the page's V scales into range. A weight times a scale is rounded to half, which holds
+  // 2^-25 to 2^16: the weights use all of that, so the scales have to stay near 1. Those of a block
+  // are taken times a power of two 2^k (exactly, but for scales below 2^-14 of the largest), which
+  // goes down when a larger scale comes: 0 for a largest scale in [2^-6, 1), else what brings it
+  // into [1/2, 1). O and the block's row of off are in units of 2^-k. NaN scales go too: 0 x NaN
+  // would reach the other blocks through the shared sum of weights; end() puts the NaN where it
+  // belongs.
+  __device__ __forceinline__ void scale_values(unsigned char* pg, int lane) {
+    constexpr int LB = 32 / NB, NW = NB / 2;         // lanes of a block, words of a lane
+    uint32_t* at = reinterpret_cast<uint32_t*>(pg + P::kVs) + lane * NW;
+    uint32_t w[NW], top = 0u;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      uint16_t* sp = reinterpret_cast<uint16_t*>(pg + P::v_scale(b, lane));
-      const uint32_t v = *sp;
-      if (__any_sync(0xffffffffu, v > 0x7c00u)) nan |= 1u << b;
-      if (v > 0x7c00u) *sp = 0;
-      else smax = max(smax, v);
+    for (int i = 0; i < NW; ++i) {
+      w[i] = at[i];
+      top = __vmaxu2(top, w[i]);
     }
-    if (nan != 0u) {
-      // 0 x NaN would reach the other blocks through the shared sum of weights, so those scales
-      // go, and end() puts the NaN where it belongs
-      poison |= nan;
-      fence_proxy_async_smem();      // the stage's next copy comes after these stores
-      __syncwarp();
+    top = max(top & 0xffffu, top >> 16);
+    // the usual first page: 2^-6 to 1 in every lane
+    if (units == kAll(kNoUnit) && __all_sync(0xffffffffu, top >= 0x2400u && top <= 0x3c00u)) {
+      units = kAll(0);
+      return;
     }
-    // 2^ev > every V scale of the page (at least 1)
-    const float ev = (float)max(0, (int)(__reduce_max_sync(0xffffffffu, smax) >> 10) - 14);
+    // 2^ev > every scale (of the lane's)
+    auto above = [](uint32_t h) {
+      return (int)(__float_as_uint(__half2float(__ushort_as_half((unsigned short)h))) >> 23) - 126;
+    };
+    int k = unit(kAt(lane / LB));
+    if (__any_sync(0xffffffffu, top > 0x7bffu || above(top) + k > 0)) {
+      uint32_t bad = 0u;
+      top = 0u;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) {
+        const uint32_t m = __vcmpgtu2(w[i], 0x7bff7bffu);
+        w[i] &= ~m;
+        bad |= m;
+        top = __vmaxu2(top, w[i]);
+      }
+      top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+      for (int o = 1; o < LB; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const uint32_t nan = __ballot_sync(0xffffffffu, bad != 0u);
+      const int ev = above(top);
+      if (ev + k > 0) k = ev >= -5 && ev <= 0 ? 0 : -ev;
+      uint32_t now = 0u;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int kb = __shfl_sync(0xffffffffu, k, b * LB);
+        now |= (uint32_t)(kb + 32) << kAt(b) | (kb != 0 ? 1u << 31 : 0u) | (units & kNan(b));
+        if (nan >> (b * LB) & ((1u << LB) - 1u)) now |= kNan(b);
+        const float f = pow2(kb - unit(kAt(b)));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          O[b][0][i] *= f;
+          O[b][1][i] *= f;
+        }
+        if (lane >> 2 == b) {
+          off[0] *= f;
+          off[1] *= f;
+        }
+      }
+      units = now;
+    }
+    const __half2 f = __float2half2_rn(pow2(k / 2)), h = __float2half2_rn(pow2(k - k / 2));
+#pragma unroll
+    for (int i = 0; i < NW; ++i) at[i] = as_u32(__hmul2(__hmul2(as_half2(w[i]), f), h));
+    fence_proxy_async_smem();        // the stage's next copy comes after these stores
+    __syncwarp();
+  }
+
+  // The references for a page whose logits over them are x, the largest in this lane's columns and
+  // rows h0, h1. x becomes relative to the new references.
+  __device__ __forceinline__ void move_reference(float (&x)[2][4], float h0, float h1) {
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {               // the 8 lanes sharing t
       h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));
       h1 = fmaxf(h1, __shfl_xor_sync(0xffffffffu, h1, o));
     }
     // the moves as the accumulators will hold them (0 where no row counts in the column yet)
-    const float u0 = advance(c0, f0, move_of(h0, ev, lim0)), u1 = advance(c1, f1, move_of(h1, ev, lim1));
+    const float u0 = advance(c0, f0, move_of(h0, lim0)), u1 = advance(c1, f1, move_of(h1, lim1));
     const float e0 = ex2_ftz((lim0 < 0.f ? lim0 : 0.f) - u0), e1 = ex2_ftz((lim1 < 0.f ? lim1 : 0.f) - u1);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -615,13 +683,12 @@ struct PageWarp<bf16, D, G> {
       for (int j = 0; j < 4; ++j) {
         // (a move far from 0 is rounded; a weight may not pass 2^15 for that)
         const float y = x[i][j] - (j & 1 ? u1 : u0);
-        x[i][j] = y > 15.f - ev ? 15.f - ev : y;     // (a NaN stays)
+        x[i][j] = y > 15.f ? 15.f : y;               // (a NaN stays)
       }
   }
 
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    constexpr float kUp = 16777216.f;
     const float r0 = -c0 * f0, r1 = -c1 * f1;        // the references are base + r
     const float m0 = base + r0, m1 = base + r1;
     if (base != 0.f) {
@@ -640,9 +707,11 @@ struct PageWarp<bf16, D, G> {
     const float l0 = __shfl_sync(0xffffffffu, off[0], 16 + t), l1 = __shfl_sync(0xffffffffu, off[1], 16 + t);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float z0 = __shfl_sync(0xffffffffu, off[0], b * 4 + t) * 8.f;
-      float z1 = __shfl_sync(0xffffffffu, off[1], b * 4 + t) * 8.f;
-      if (poison >> b & 1u) z0 = z1 = NAN;
+      const int k = unit(kAt(b));
+      const float kUp = pow2(24 - k), kOff = pow2(3 - k);
+      float z0 = __shfl_sync(0xffffffffu, off[0], b * 4 + t) * kOff;
+      float z1 = __shfl_sync(0xffffffffu, off[1], b * 4 + t) * kOff;
+      if (units & kNan(b)) z0 = z1 = NAN;
       const float(&X)[4] = O[b][0], (&Y)[4] = O[b][1];
       if (2 * t < G)
         *reinterpret_cast<float4*>(sa + 2 * t * D + b * 32 + g * 4) =

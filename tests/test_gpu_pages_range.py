@@ -13,9 +13,9 @@ row with a weight has:
          times scale, whose error counts on a code u <= 15; below the half range both are off by half
          a subnormal step, 2^-25, the largest weight being at least 2^7: n 2^-32 2 |v| for the
          weights, and n 2^-32 15 U for their products with the scales, which a warp holds in units of
-         U >= 2^-k of its block: 1 while the largest scale of the block lies in (2^-6, 1], else the
-         power of two above that scale (so at most twice it); scales above 1 are brought down to
-         that unit and may leave the half range there: 7 2^-25 U; and 2^-8 |out| for the output.
+         at most U for each block of channels: 1 for a largest scale of the block in [2^-6, 1), else
+         the power of two above that scale (at most twice it); scales far below that unit may leave
+         the half range: 7 2^-25 U; and 2^-8 |out| for the output.
 """
 
 import gc
@@ -103,7 +103,7 @@ class Units:
             if self.dtype == torch.bfloat16:
                 s = self.scales(u).repeat_interleave(32, 1)
                 top = s.max(0).values
-                unit = torch.where((top > 2.0 ** -6) & (top <= 1), 1.0, 2 * top)
+                unit = torch.where((top >= 2.0 ** -6) & (top < 1), 1.0, 2 * top)
                 bound += 2.0 ** -11 * (size + want.abs()) + 15 * 2.0 ** -11 * (w @ s) + 2.0 ** -8 * want.abs()
                 bound += T * 2.0 ** -32 * (2 * v.abs().max(0).values + 15 * unit) + 7 * 2.0 ** -25 * unit
             err = (out[u] - want).abs()
@@ -164,4 +164,42 @@ def test_logits_count_beside_a_far_log_count_that_all_rows_have(kvs, dtype, shap
     c.logn[:] = low
     c.store()
     q = c.queries(8.0)
+    c.check(q, c.decode(q))
+
+
+LONG = [(160, 8192, 0), (8, 16384 + 64, 0), (8, 8192, 5000), (2, 30000, 1100)]
+
+
+def heavy(c, nats):
+    """One row in 2048 that many nats above the others."""
+    c.logn[:] = torch.where(torch.arange(c.T, device=DEV) % 2048 == 5, nats, 0.0)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("units,T,wide", LONG, ids=["many", "cluster", "split", "clusters"])
+@pytest.mark.parametrize("v_scale", [1e-6, 1e-5, 3e-5, 1e-4, 1e-3, 1e-2, 30.0, 1e3, 6e4])
+def test_values_of_every_size(kvs, dtype, units, T, wide, v_scale):
+    c = Units(kvs, units, T, 2, 64, dtype, seed=4, v_scale=v_scale, wide=wide)
+    heavy(c, 10.0)
+    c.store()
+    q = c.queries(1.0)
+    c.check(q, c.decode(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("units,T,wide", LONG, ids=["many", "cluster", "split", "clusters"])
+@pytest.mark.parametrize("down", [False, True])
+def test_values_whose_size_changes(kvs, dtype, units, T, wide, down):
+    """Blocks of channels of their own sizes, two of them growing (or shrinking) along the rows and
+    one zero for the first half."""
+    c = Units(kvs, units, T, 4, 128, dtype, seed=5, wide=wide)
+    ramp = torch.linspace(-20, 14, T, device=DEV)
+    ramp = torch.exp2(ramp.flip(0) if down else ramp)[:, None]
+    c.V[..., :32] *= ramp
+    c.V[..., 32:64] *= 3e-6
+    c.V[..., 64:96] *= 2.0 ** -10 * ramp
+    c.V[:, :, :T // 2, 96:] = 0
+    heavy(c, 10.0)
+    c.store()
+    q = c.queries(1.0)
     c.check(q, c.decode(q))
