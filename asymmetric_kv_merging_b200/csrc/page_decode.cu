@@ -184,11 +184,13 @@ struct PageWarp {
 #pragma unroll
       for (int g = 0; g < G; ++g) x[g] = fmaf(y[g].x + y[g].y, s, x[g]);
     }
+    // rows that count: one whose log-count is -inf does not, whatever it holds
     const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane)) * kLog2e;
+    const uint32_t live = __ballot_sync(0xffffffffu, lane < nval && ln != -INFINITY);
     float p[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float xg = lane < nval ? x[g] + ln : -INFINITY;
+      const float xg = live >> lane & 1u ? x[g] + ln : -INFINITY;
       if (__any_sync(0xffffffffu, xg > m[g])) {      // a new maximum: rare after the first pages
         const float M = fmaxf(m[g], warp_max(xg));
         const float f = exp2f(m[g] - M);
@@ -206,8 +208,8 @@ struct PageWarp {
       const int r = r0 + 2 * (lane / QL);
       const uint32_t w = *reinterpret_cast<const uint32_t*>(pg + P::v_piece(b, r, quad % 8));
       float2 s = __half22float2(*reinterpret_cast<const __half2*>(pg + P::v_scale(b, r)));
-      if (r >= nval) s.x = 0.f;                      // whatever the rest of the page holds
-      if (r + 1 >= nval) s.y = 0.f;
+      if (!(live >> r & 1u)) s.x = 0.f;              // (also what the rest of the page holds)
+      if (!(live >> r & 2u)) s.y = 0.f;
       float v[8];
       centred8(w, v);
 #pragma unroll
@@ -495,7 +497,7 @@ struct PageWarp<bf16, D, G> {
       __syncwarp();
     }
     float x[2][4];
-    for (bool again = false;; again = true) {
+    for (bool again = false;;) {
       logits(pg, lane, x);
       // The reference of a column moves only when a weight would pass 2^15, to where the largest is
       // 2^7: after the first pages that is rare. Scales out of range are rare too: above 1 (adding
@@ -508,14 +510,17 @@ struct PageWarp<bf16, D, G> {
       } else {
         odd |= *reinterpret_cast<const uint32_t*>(pg + P::kVs + lane * 4) + 0x43ff43ffu;
       }
-      const float h0 = fmaxf(max3(x[0][0], x[0][2], x[1][0]), x[1][2]);
-      const float h1 = fmaxf(max3(x[0][1], x[0][3], x[1][1]), x[1][3]);
-      const bool far = h0 > lim0 || h1 > lim1;
+      const float h0 = max_nan(max3_nan(x[0][0], x[0][2], x[1][0]), x[1][2]);
+      const float h1 = max_nan(max3_nan(x[0][1], x[0][3], x[1][1]), x[1][3]);
+      const bool far = !(h0 <= lim0 && h1 <= lim1);        // (a NaN too)
       if (!again && !__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u || far)) break;
       const bool move = again || __any_sync(0xffffffffu, far);
-      if (move && !again && move_base(pg, lane)) continue;       // the logits are made anew
+      if (move && !again && move_base(pg, lane)) {
+        again = true;                                      // the logits are made anew
+        continue;
+      }
       if (__any_sync(0xffffffffu, (odd & 0x80008000u) != 0u)) scale_values(pg, lane);
-      if (move) move_reference(x, h0, h1);
+      if (move) move_reference(pg, x, h0, h1, lane);
       break;
     }
     __half2 pb[2][2];
@@ -552,6 +557,12 @@ struct PageWarp<bf16, D, G> {
         mma_f16_16816(O[b][1], ua & LO, ua, ub & LO, ub, w0, w1);
       }
     }
+  }
+
+  // A row whose log-count is -inf is left out whatever it holds: where keys or values read as NaN,
+  // move_reference and scale_values ask for it.
+  static __device__ __forceinline__ bool masked(const unsigned char* pg, int r) {
+    return __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e) == -INFINITY;
   }
 
   // A log-count (log2) further than this above the base becomes the new base: its distance to the
@@ -620,6 +631,9 @@ struct PageWarp<bf16, D, G> {
       top = 0u;
 #pragma unroll
       for (int i = 0; i < NW; ++i) {
+        const int r = (lane % LB * NW + i) * 2;
+        if (masked(pg, r)) w[i] &= 0xffff0000u;
+        if (masked(pg, r + 1)) w[i] &= 0xffffu;
         const uint32_t m = __vcmpgtu2(w[i], 0x7bff7bffu);
         w[i] &= ~m;
         bad |= m;
@@ -658,8 +672,18 @@ struct PageWarp<bf16, D, G> {
   }
 
   // The references for a page whose logits over them are x, the largest in this lane's columns and
-  // rows h0, h1. x becomes relative to the new references.
-  __device__ __forceinline__ void move_reference(float (&x)[2][4], float h0, float h1) {
+  // rows h0, h1 (NaN if one is). x becomes relative to the new references.
+  __device__ __forceinline__ void move_reference(const unsigned char* pg, float (&x)[2][4], float h0, float h1,
+                                                 int lane) {
+    if (__any_sync(0xffffffffu, h0 != h0 || h1 != h1)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+          if (masked(pg, i * 16 + (lane >> 2) + j * 4)) x[i][j] = x[i][j + 1] = -INFINITY;
+      h0 = fmaxf(fmaxf(x[0][0], x[0][2]), fmaxf(x[1][0], x[1][2]));
+      h1 = fmaxf(fmaxf(x[0][1], x[0][3]), fmaxf(x[1][1], x[1][3]));
+    }
 #pragma unroll
     for (int o = 4; o < 32; o <<= 1) {               // the 8 lanes sharing t
       h0 = fmaxf(h0, __shfl_xor_sync(0xffffffffu, h0, o));

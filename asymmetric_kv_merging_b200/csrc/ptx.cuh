@@ -449,10 +449,15 @@ __device__ __forceinline__ float ex2_ftz(float x) {
   return y;
 }
 
-// Maximum of three (sm_100; a NaN operand is ignored).
-__device__ __forceinline__ float max3(float a, float b, float c) {
+// Maximum of two and of three (sm_100), NaN if one is.
+__device__ __forceinline__ float max_nan(float a, float b) {
   float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 

@@ -418,7 +418,7 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * without the new row): reserve the row with kvs_page_assign first. A unit with nothing to
  * attend gets zeros. Rows whose page number is outside the pool are skipped
  * (KVS_FLAG_BAD_PAGE). A log-count of -inf, or one below -2.3e38 (its product with log2 e is
- * -inf), leaves its row out. T_cap of desc is not used (any valid value). Two units may share a
+ * -inf), leaves its row out, whatever it holds. T_cap of desc is not used (any valid value). Two units may share a
  * page that neither appends to.
  * Rounding: fp32 descriptors compute in fp32 throughout; with bf16 the softmax weights are
  * rounded to half precision (2^-11), alone and times a row's scale, and queries are below

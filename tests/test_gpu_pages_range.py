@@ -87,11 +87,11 @@ class Units:
         s = self.pages[at, 34 * self.d:36 * self.d].view(torch.float16).view(len(at), -1, PAGE)
         return s.transpose(1, 2).reshape(-1, self.d // 32)[:self.T].double()
 
-    def check(self, q, out, extra=0.0):
-        """`extra`: what log-counts of rows without a weight add to X."""
+    def check(self, q, out, extra=0.0, but=None):
+        """`extra`: what log-counts of rows without a weight add to X. `but`: a unit to leave out."""
         d, T, worst = self.d, self.T, 0.0
         q, out = (x.view(self.units, self.G, d).double() for x in (q, out))
-        for u in range(self.units):
+        for u in [u for u in range(self.units) if u != but]:
             k, v, ln = self.K[0, u].double(), self.V[0, u].double(), self.logn[0, u].double()
             ln = ln - ln.max()                               # the same softmax, and exact
             w = torch.softmax(q[u] @ k.T / d ** 0.5 + ln, -1)
@@ -101,7 +101,7 @@ class Units:
             bound = (2 * (d + 6) * 2.0 ** -24 * x + (T + 16) * 2.0 ** -24 + 2.0 ** -21) * size
             bound += 2.0 ** -24 * want.abs()
             if self.dtype == torch.bfloat16:
-                s = self.scales(u).repeat_interleave(32, 1)
+                s = torch.where(live[:, None], self.scales(u).repeat_interleave(32, 1), 0)
                 top = s.max(0).values
                 unit = torch.where((top >= 2.0 ** -6) & (top < 1), 1.0, 2 * top)
                 bound += 2.0 ** -11 * (size + want.abs()) + 15 * 2.0 ** -11 * (w @ s) + 2.0 ** -8 * want.abs()
@@ -203,3 +203,30 @@ def test_values_whose_size_changes(kvs, dtype, units, T, wide, down):
     c.store()
     q = c.queries(1.0)
     c.check(q, c.decode(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("units,T,wide", LONG, ids=["many", "cluster", "split", "clusters"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("low", [-float("inf"), torch.finfo(torch.float32).min])
+def test_rows_left_out_may_hold_nan(kvs, dtype, units, T, wide, d, low):
+    """Rows with a log-count of -inf (or one whose product with log2 e is) hold NaN or infinite keys
+    or values, alone, by pages and, in unit 1, throughout."""
+    c = Units(kvs, units, T, 2, d, dtype, seed=6, wide=wide)
+    t = torch.arange(T, device=DEV)
+    off = [t % 7 == 3, t % 11 == 5, t // PAGE % 5 == 4]
+    c.K[:, :, off[0], 1] = float("nan")
+    c.V[:, :, off[1], d - 1] = -float("inf")
+    c.K[:, :, off[2]] = float("inf")
+    c.V[:, :, off[2]] = float("nan")
+    gone = off[0] | off[1] | off[2]
+    c.K[0, 1, :, 40], c.V[0, 1, :, 3] = float("nan"), float("nan")
+    c.logn[:, :, gone] = low
+    c.logn[0, 1] = low
+    c.store()
+    for x in (c.K, c.V):
+        x[:, :, gone] = 0                                    # (for the oracle)
+    q = c.queries(1.0)
+    out = c.decode(q).view(units, 2, d)
+    assert not out[1].any()
+    c.check(q, out, but=1)
