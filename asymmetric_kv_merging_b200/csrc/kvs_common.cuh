@@ -179,12 +179,17 @@ inline int decode_splits(const kvs_cache_desc& d) {
 }
 
 // Every layout starts with the same persistent region: the device flag word in the
-// first 256 bytes, then one arrival counter per KV head for the decode combine. No
-// op writes this region except through its own flags / counters, so one zeroed
-// workspace can be shared by all ops on a stream.
-inline size_t persistent_bytes(const kvs_cache_desc& d) {
-  return kWsAlign + align_up((size_t)d.B * d.H_kv * sizeof(int32_t), kWsAlign);
+// first 256 bytes, the arrival counters of the paged decode (one per CTA, whatever the
+// shape), then one arrival counter per KV head for the decode combine. No op writes
+// this region except through its own flags / counters, so one zeroed workspace can be
+// shared by all ops on a stream. (Scratch of a shape with fewer heads begins where a
+// larger one has its last head counters; the paged decode's lie before all of them.)
+constexpr int kPageDecodeCtas = kTargetCtas;
+constexpr size_t kHeadCounters = kWsAlign + (kPageDecodeCtas * sizeof(int32_t) + kWsAlign - 1) / kWsAlign * kWsAlign;
+inline size_t persistent_bytes(size_t heads) {
+  return kHeadCounters + align_up(heads * sizeof(int32_t), kWsAlign);
 }
+inline size_t persistent_bytes(const kvs_cache_desc& d) { return persistent_bytes((size_t)d.B * d.H_kv); }
 
 inline ScoreLayout score_layout(const kvs_cache_desc& d, int W) {
   ScoreLayout L;
@@ -226,7 +231,7 @@ inline DecodeLayout decode_layout(const kvs_cache_desc& d) {
   DecodeLayout L;
   size_t qheads = (size_t)d.B * d.H_q;
   L.nsplit = decode_splits(d);
-  L.counters = kWsAlign;
+  L.counters = kHeadCounters;
   L.part = persistent_bytes(d);
   L.total = align_up(L.part + qheads * L.nsplit * (size_t)(d.d + kPartPad) * sizeof(float),
                      kWsAlign);
@@ -235,17 +240,14 @@ inline DecodeLayout decode_layout(const kvs_cache_desc& d) {
 
 // The 4-bit paged cache. The decode's work split gives every CTA of one wave (two per SM) an
 // equal run of pages, so a CTA leaves at most two partial rows per query head: one of a unit
-// that began before it, one of a unit that goes on after it. `done` counts the CTAs that are
-// through with the lengths (inside the flag word's block). The scratch (`part` bytes) lies at the
-// end of the workspace, so that calls with fewer units leave the counters of larger ones alone.
-constexpr int kPageDecodeCtas = kTargetCtas;
+// that began before it, one of a unit that goes on after it; the unit's arrivals are counted at the
+// CTA that it begins in. `done` counts the CTAs that are through with the lengths (inside the flag
+// word's block). The scratch (`part` bytes) lies at the end of the workspace, so that calls with
+// fewer units leave the head counters of larger ones alone.
 struct PageLayoutWs {
   size_t done, counters, part, total;
 };
 
-inline size_t page_persistent_bytes(int units) {
-  return kWsAlign + align_up((size_t)units * sizeof(int32_t), kWsAlign);
-}
 // Where the last `bytes` (a multiple of kWsAlign) of a workspace begin.
 inline size_t ws_tail(size_t ws_bytes, size_t bytes) { return ws_bytes / kWsAlign * kWsAlign - bytes; }
 
@@ -258,7 +260,7 @@ inline PageAssignWs page_assign_ws(int units) {
   PageAssignWs L;
   L.done = kWsAlign * 3 / 4;
   L.scratch = align_up(16 + (size_t)units * 2 * sizeof(int32_t), kWsAlign);
-  L.total = page_persistent_bytes(units) + L.scratch;
+  L.total = persistent_bytes((size_t)units) + L.scratch;
   return L;
 }
 
@@ -268,7 +270,7 @@ inline PageLayoutWs page_layout_ws(const kvs_cache_desc& d) {
   L.done = kWsAlign / 2;
   L.counters = kWsAlign;
   L.part = align_up((size_t)kPageDecodeCtas * 2 * (d.H_q / d.H_kv) * (d.d + kPartPad) * sizeof(float), kWsAlign);
-  L.total = page_persistent_bytes(units) + L.part;
+  L.total = persistent_bytes(d) + L.part;
   if (L.total < page_assign_ws(units).total) L.total = page_assign_ws(units).total;
   return L;
 }

@@ -23,7 +23,8 @@
 
 namespace {
 
-constexpr size_t kStaticScratchBytes = 4u << 20;   // 4 MiB
+// 4 MiB, and what the paged decode's counters take of every layout
+constexpr size_t kStaticScratchBytes = (4u << 20) + kvs::kHeadCounters - kvs::kWsAlign;
 constexpr int kMaxDevices = 64;
 
 __device__ __align__(256) unsigned char g_decode_scratch[kStaticScratchBytes];

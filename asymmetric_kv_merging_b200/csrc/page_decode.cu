@@ -11,7 +11,7 @@
 //    itself. The pages of all units (KV heads of all sequences) are numbered one unit after
 //    another and dealt out in even runs, or a fixed number of CTAs goes to each unit. A unit that
 //    lies in one CTA is finished there; one that spans several gets a partial row per CTA in the
-//    workspace, and the last of them to arrive (a counter per unit) combines. No CTA waits for
+//    workspace, and the last of them to arrive (a counter at the first of them) combines. No CTA waits for
 //    another.
 //  - cluster kernel: one thread-block cluster per unit, combined in distributed shared memory (one
 //    or two units with wide tables: several, joined through the workspace).
@@ -102,6 +102,7 @@ static bool use_cluster(int C, int clusters, int max_pages) {
 // trip costs 1.6 us. The table's width decides, not a length: a unit's CTAs could read different
 // lengths once one of them has appended.
 constexpr int kPcWide = 1024;
+static_assert(8 * kMaxClusterSize <= kPageDecodeCtas, "a counter for every slice");
 static int clusters_of(int units, int max_pages) {
   return units <= 2 && max_pages > kPcWide ? 8 / units : 1;
 }
@@ -853,7 +854,7 @@ struct PageArgs {
   const T* v_new;
   T* out;
   int units;
-  int32_t* counters;
+  int32_t* counters;           // [kPageDecodeCtas]
   int32_t* done;
   float* part;
   int32_t* flags;
@@ -1178,7 +1179,7 @@ page_decode_kernel(const PageArgs<T> a) {
     __syncthreads();
     if (tid < 2) {
       const int4 sp = s_split[tid];
-      s_last[tid] = sp.x >= 0 && atom_add_acq_rel_gpu(&a.counters[sp.x], 1) == sp.z - 1;
+      s_last[tid] = sp.x >= 0 && atom_add_acq_rel_gpu(&a.counters[sp.y], 1) == sp.z - 1;
     }
     int new_id[2];                                 // (loads that overlap the arrivals')
 #pragma unroll
@@ -1230,7 +1231,7 @@ page_decode_kernel(const PageArgs<T> a) {
                             a.out + (size_t)u * G * D + tid * 4);
         }
         append(u, sp.w, id);
-        if (tid == 0) a.counters[u] = 0;
+        if (tid == 0) a.counters[sp.y] = 0;
         continue;
       }
       float* fac = s_acc;                          // [G][np]
@@ -1296,7 +1297,7 @@ page_decode_kernel(const PageArgs<T> a) {
                           a.v_new + (size_t)u * D + c, a.out + (size_t)u * G * D + unit * 4);
       }
       append(u, sp.w, id);
-      if (tid == 0) a.counters[u] = 0;
+      if (tid == 0) a.counters[sp.y] = 0;
       __syncthreads();            // the shared arrays are free for the other unit
     }
   }

@@ -91,7 +91,7 @@ static cudaError_t launch_append_t(const kvs_cache_desc& d, void* K, void* V, fl
   dim3 grid((n + kAppendRowsPerBlock - 1) / kAppendRowsPerBlock, d.B * d.H_kv);
   append_rows_kernel<T, D><<<grid, kAppendThreads, 0, st>>>(
       (T*)K, (T*)V, logn, len, L, (const T*)k_rows, (const T*)v_rows, n, d.T_cap,
-      reinterpret_cast<int32_t*>(ws + kWsAlign), reinterpret_cast<int32_t*>(ws));
+      reinterpret_cast<int32_t*>(ws + kHeadCounters), reinterpret_cast<int32_t*>(ws));
   count_launches(1);
   return cudaGetLastError();
 }

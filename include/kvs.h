@@ -97,12 +97,18 @@ enum {
 /*
  * Bytes of workspace `op` needs for caches of shape `desc` (and window W for
  * KVS_OP_SCORE). Returns 0 for an invalid shape. Every layout begins with the
- * same persistent region: the device flag word (first 256 bytes) and one decode
- * arrival counter per KV head (the next 256-byte-aligned block). Zero the whole
- * workspace once (cudaMemset) before its first use; every call leaves the
- * persistent region valid for the next call, so one zeroed workspace, sized for
- * the largest op, serves all three ops on one stream. Calls that share a
- * workspace must not overlap in time.
+ * same persistent region: the device flag word (first 256 bytes), the arrival
+ * counters of the paged decode (as many for every shape) and one decode arrival
+ * counter per KV head. Zero the whole workspace once (cudaMemset) before its first
+ * use; every call leaves the persistent region valid for the next call of its shape,
+ * so one zeroed workspace, sized for the largest op, serves all ops on one stream.
+ * Calls that share a workspace must not overlap in time.
+ * Shapes may differ too, if the workspace is sized for the largest B * H_kv among them
+ * for every op in use (and the largest W, T_cap, d and H_q / H_kv), with one exception:
+ * scratch of a shape with fewer heads overwrites counters that kvs_decode_attn and
+ * kvs_prefill_chunk have for one with more, so for those two give each B * H_kv a
+ * workspace of its own. The paged calls (kvs_page_*) may follow, and be followed by,
+ * calls of any shape.
  */
 size_t kvs_workspace_size(const kvs_cache_desc* desc, int32_t W, int32_t op);
 
@@ -288,7 +294,7 @@ kvs_status kvs_decode_attn(const kvs_cache_desc* desc, const void* q, void* K, v
  *
  * It computes exactly what kvs_decode_attn computes (same kernels, same arguments
  * minus ws / ws_bytes) using a scratch buffer built into the library: a device
- * array of kvs_static_scratch_bytes() bytes (4 MiB) that every GPU which loads the
+ * array of kvs_static_scratch_bytes() bytes (4 MiB and 1280 bytes) that every GPU which loads the
  * library holds until the process exits. Shapes whose decode workspace
  * (kvs_workspace_size(desc, 0, KVS_OP_DECODE)) exceeds it return KVS_ERR_WORKSPACE
  * and launch nothing. It allocates nothing: no cudaMalloc, no cudaFree.
@@ -428,7 +434,8 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
  * Workspace: kvs_workspace_size(desc, 0, KVS_OP_PAGES) bytes; its counters must be zero at
  * the first call (each call leaves them zero). One that is sized for the largest B serves
- * every smaller one too (same heads and d), in any order. Make the first call for a device
+ * every smaller one too (same heads and d), in any order, with calls of other ops in
+ * between (kvs_workspace_size). Make the first call for a device
  * outside any stream capture (it sets kernel attributes and asks the occupancy calculator).
  * Few units with short tables are decoded by a cluster of CTAs each, one or two with long
  * ones by several, other calls by CTAs that split all pages among them; the same call gives
