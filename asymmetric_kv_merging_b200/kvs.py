@@ -137,8 +137,13 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-# the handle of a device's current stream without building a Stream object (3 us a call)
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the handle of a device's current stream without building a Stream object (3 us a call), where torch
+# has it: one without CUDA does not, and sizes and plans need no device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 _current_device = torch.cuda.current_device
 
 
