@@ -375,8 +375,8 @@ size_t kvs_page_bytes(int32_t d);
  * A unit whose rows or held is out of range is left as it is (KVS_FLAG_BAD_LENGTH).
  *
  * Slot map (when slots is given): slots[u][i] = 32 * page + row of row slot_begin[u] + i of
- * unit u for i < slot_stride, or -1 where that row is not below rows[u] or has no page.
- * kvs_page_store and kvs_page_load take it.
+ * unit u for i < slot_stride, or -1 where that row is not below rows[u] or has no page (or
+ * one outside the pool: KVS_FLAG_BAD_PAGE). kvs_page_store and kvs_page_load take it.
  *
  * In:  pool (table updated; pages not touched), rows [units], slot_begin [units] (nullable:
  *      0 everywhere).
