@@ -122,6 +122,17 @@ __device__ __forceinline__ int unit_span(int L) { return pages_of(L) + kUnitPage
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
+// A log-count (log2) further than this from what a warp's logits are relative to moves that: its
+// distance to the ones that matter then costs a logit 2^-14 at most.
+constexpr float kFarLogn = 1024.f;
+
+// What the sum s = a + b has lost to rounding, log2 of a factor for the weights whose reference s is.
+// Within 64, so that sums of weights times values stay in fp32; only logits of more than 49 beside
+// log-counts of more than 1.4e9 pass that.
+__device__ __forceinline__ float sum_residual(float a, float b, float s) {
+  return fminf(fmaxf((a - s) + b, -64.f), 64.f);
+}
+
 // One warp's share of a unit: its softmax state over the pages it has taken. load() and prepare()
 // make the unit's operands from its queries (share() and fetch() hand them from one warp to the
 // others), reset() starts a unit, take() adds the first nval rows of a page, end() writes the
@@ -136,6 +147,9 @@ struct PageWarp {
   using P = PageLayout<D>;
   static constexpr int QL = D / 4, RPS = 32 / QL;       // lanes per row of V, rows at a time
   const float (*qs)[D];        // scaled queries, in shared memory
+  // log-counts (log2) are taken relative to `base`, so that logits count beside ones that are far
+  // from zero throughout; so are the maxima
+  float base;
   float m[G], l[G];
   float2 acc[G][2];
 
@@ -149,6 +163,7 @@ struct PageWarp {
   }
   __device__ __forceinline__ void fetch(const void* from, int) { qs = reinterpret_cast<const float(*)[D]>(from); }
   __device__ __forceinline__ void reset() {
+    base = 0.f;
 #pragma unroll
     for (int g = 0; g < G; ++g) {
       m[g] = -INFINITY;
@@ -187,11 +202,23 @@ struct PageWarp {
     }
     // rows that count: one whose log-count is -inf does not, whatever it holds
     const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane)) * kLog2e;
-    const uint32_t live = __ballot_sync(0xffffffffu, lane < nval && ln != -INFINITY);
+    const bool counts = lane < nval && ln != -INFINITY;
+    const uint32_t live = __ballot_sync(0xffffffffu, counts);
+    if (__any_sync(0xffffffffu, counts && fabsf(ln - base) > kFarLogn)) {
+      const float top = redux_max(counts ? ln : -INFINITY);
+      bool none = true;
+#pragma unroll
+      for (int g = 0; g < G; ++g) none = none && m[g] == -INFINITY;
+      if (fabsf(top) < INFINITY && (top - base > kFarLogn || (none && base - top > kFarLogn))) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) m[g] += base - top;
+        base = top;
+      }
+    }
     float p[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float xg = live >> lane & 1u ? x[g] + ln : -INFINITY;
+      const float xg = counts ? x[g] + (ln - base) : -INFINITY;
       if (__any_sync(0xffffffffu, xg > m[g])) {      // a new maximum: rare after the first pages
         const float M = fmaxf(m[g], warp_max(xg));
         const float f = exp2f(m[g] - M);
@@ -233,12 +260,14 @@ struct PageWarp {
   __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float ls = warp_sum(l[g]);
+      const float M = base + m[g];
+      const float f = base == 0.f ? 1.f : exp2f(sum_residual(base, m[g], M));
+      const float ls = warp_sum(l[g]) * f;
       if (lane == 0) {
-        sm[g] = m[g];
+        sm[g] = M;
         sl[g] = ls;
       }
-      float4 v = make_float4(acc[g][0].x, acc[g][0].y, acc[g][1].x, acc[g][1].y);
+      float4 v = make_float4(acc[g][0].x * f, acc[g][0].y * f, acc[g][1].x * f, acc[g][1].y * f);
       if (RPS == 2) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
@@ -566,24 +595,20 @@ struct PageWarp<bf16, D, G> {
     return __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e) == -INFINITY;
   }
 
-  // A log-count (log2) further than this above the base becomes the new base: its distance to the
-  // ones that matter then costs a logit 2^-14 at most.
-  static constexpr float kFar = 1024.f;
-
   // Takes the base to the page's largest log-count if that is far above it, or if it is far below
   // and no row has counted yet. The old reference, which the new logits would be lost against, is
   // left in lim (relative to the new base, so far below 0) for move_reference to join with them.
   __device__ __forceinline__ bool move_base(const unsigned char* pg, int lane) {
     const float top = redux_max(__fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(lane)), kLog2e));
-    if (!(fabsf(top - base) > kFar)) return false;
+    if (!(fabsf(top - base) > kFarLogn)) return false;
     if (fabsf(top) == INFINITY || (top < base && __any_sync(0xffffffffu, fmaxf(lim0, lim1) > 0.f))) return false;
     const float r0 = (base - top) - c0 * f0, r1 = (base - top) - c1 * f1;
     base = top;
     // a reference that logits put so high that it is near the new base, or above it, stays
-    c0 = lim0 > 0.f && r0 > -kFar ? -r0 / f0 : 0.f;
-    c1 = lim1 > 0.f && r1 > -kFar ? -r1 / f1 : 0.f;
-    if (lim0 > 0.f && r0 <= -kFar) lim0 = r0;
-    if (lim1 > 0.f && r1 <= -kFar) lim1 = r1;
+    c0 = lim0 > 0.f && r0 > -kFarLogn ? -r0 / f0 : 0.f;
+    c1 = lim1 > 0.f && r1 > -kFarLogn ? -r1 / f1 : 0.f;
+    if (lim0 > 0.f && r0 <= -kFarLogn) lim0 = r0;
+    if (lim1 > 0.f && r1 <= -kFarLogn) lim1 = r1;
     return true;
   }
 
@@ -717,10 +742,7 @@ struct PageWarp<bf16, D, G> {
     const float r0 = -c0 * f0, r1 = -c1 * f1;        // the references are base + r
     const float m0 = base + r0, m1 = base + r1;
     if (base != 0.f) {
-      // what the sum's rounding has lost goes into the sums (up to 2^100, which only logits of
-      // more than 70 beside log-counts of more than 1e9 pass)
-      const float e0 = ex2_ftz(fminf(fmaxf((base - m0) + r0, -100.f), 100.f));
-      const float e1 = ex2_ftz(fminf(fmaxf((base - m1) + r1, -100.f), 100.f));
+      const float e0 = ex2_ftz(sum_residual(base, r0, m0)), e1 = ex2_ftz(sum_residual(base, r1, m1));
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll

@@ -230,3 +230,13 @@ def test_rows_left_out_may_hold_nan(kvs, dtype, units, T, wide, d, low):
     out = c.decode(q).view(units, 2, d)
     assert not out[1].any()
     c.check(q, out, but=1)
+
+
+@pytest.mark.parametrize("low", LOW + [1e6, 1e9, 1e30])
+def test_fp32_logits_count_beside_a_far_log_count_that_all_rows_have(kvs, shape, low):
+    units, wide = shape
+    c = Units(kvs, units, 4096, 4, 128, torch.float32, seed=7, wide=wide)
+    c.logn[:] = low
+    c.store()
+    q = c.queries(4.0)
+    c.check(q, c.decode(q))
