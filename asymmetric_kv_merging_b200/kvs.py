@@ -332,9 +332,16 @@ def page_assign(pool, rows, held, free_pages, n_free, ws, slots=None, slot_begin
         raise KvsError(st, "kvs_page_assign")
 
 
+def _dtype(desc: CacheDesc, where: str) -> torch.dtype:
+    dtype = _DTYPES.get(desc.dtype)
+    if dtype is None:
+        raise KvsError(2, where)                             # KVS_ERR_UNSUPPORTED, as the library says
+    return dtype
+
+
 def page_store(desc, K, V, logn, slots, pool, ws, stream=None):
     """kvs_page_store: the rows of K, V [B, H_kv, T_cap, d] into the pages at `slots`."""
-    d, dtype = desc.d, _DTYPES[desc.dtype]
+    d, dtype = desc.d, _dtype(desc, "kvs_page_store")
     rows = desc.B * desc.H_kv * desc.T_cap
     dev = _pool_device(pool, 0, d)
     nws = ws.numel()
@@ -348,7 +355,7 @@ def page_store(desc, K, V, logn, slots, pool, ws, stream=None):
 
 def page_load(desc, pool, slots, K, V, logn, ws, stream=None):
     """kvs_page_load: the rows at `slots` back into K, V [B, H_kv, T_cap, d] and logn."""
-    d, dtype = desc.d, _DTYPES[desc.dtype]
+    d, dtype = desc.d, _dtype(desc, "kvs_page_load")
     rows = desc.B * desc.H_kv * desc.T_cap
     dev = _pool_device(pool, 0, d)
     nws = ws.numel()
@@ -362,7 +369,7 @@ def page_load(desc, pool, slots, K, V, logn, ws, stream=None):
 
 def page_decode_attn(desc, q, pool, lens, out, ws, k_new=None, v_new=None, stream=None):
     """kvs_page_decode_attn: one decode step over the pages of every unit."""
-    d, dtype, units = desc.d, _DTYPES[desc.dtype], desc.B * desc.H_kv
+    d, dtype, units = desc.d, _dtype(desc, "kvs_page_decode_attn"), desc.B * desc.H_kv
     dev = _pool_device(pool, units, d)
     n, nws = desc.B * desc.H_q * d, ws.numel()
     st = _lib.kvs_page_decode_attn(
