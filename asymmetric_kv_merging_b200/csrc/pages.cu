@@ -181,9 +181,12 @@ page_assign_kernel(const int32_t* __restrict__ rows, int32_t* held, int32_t* tab
           if (j != j_of) {
             j_of = j;
             id = page(j);
+            if (id >= n_pages) {                           // (its slots would wrap around)
+              set_flag(flags, KVS_FLAG_BAD_PAGE);
+              id = -1;
+            }
           }
-          if (id >= n_pages) set_flag(flags, KVS_FLAG_BAD_PAGE);     // (its slots would wrap around)
-          else if (id >= 0) out[k] = id * kPageRows + (int)((unsigned)t % kPageRows);
+          if (id >= 0) out[k] = id * kPageRows + (int)((unsigned)t % kPageRows);
         }
       }
       int32_t* o = slots + (size_t)u * stride + i0;
