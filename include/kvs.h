@@ -426,9 +426,13 @@ kvs_status kvs_page_load(const kvs_cache_desc* desc, const kvs_page_pool* pool,
  * (KVS_FLAG_BAD_PAGE). A log-count of -inf, or one below -2.3e38 (its product with log2 e is
  * -inf), leaves its row out, whatever it holds. T_cap of desc is not used (any valid value). Two units may share a
  * page that neither appends to.
+ * Other log-counts may lie anywhere (-1e9 for a mask, say): rows of one unit keep their weights
+ * relative to one another.
  * Rounding: fp32 descriptors compute in fp32 throughout; with bf16 the softmax weights are
- * rounded to half precision (2^-11), alone and times a row's scale, and queries are below
- * 2^117 in magnitude (one above it makes its head's output NaN).
+ * rounded to half precision (2^-11, or 2^-32 of the largest weight where that is more), alone
+ * and times a row's scale (2^-11, or 2^-26 of the largest weight times the largest scale of the
+ * channel block), and queries are below 2^117 in magnitude (one above it makes its head's
+ * output NaN).
  * In:  q [B,H_q,d]; pool; len [B*H_kv], 0 <= len <= 32 max_pages;
  *      B * H_kv * (max_pages + 64) < 2^31.
  * Out: out [B,H_q,d] (desc's type); pages and len updated when appending.
