@@ -69,6 +69,32 @@ __device__ __forceinline__ float part_weight(float m, float l, float M) {
   return l != 0.f ? ex2_ftz(m - M) : 0.f;
 }
 
+// Log-counts are taken relative to a `base`, one of a page that the warp has met, so that neither
+// logits nor differences of log-counts are lost beside ones far from zero. One further than this
+// from the base moves it: the distance to those that matter then costs a logit 2^-14 at most.
+constexpr float kFarLogn = 710.f;
+
+__device__ __forceinline__ float logn_over(float ln, float base) { return (ln - base) * kLog2e; }
+// Whether a log-count leaves its row out.
+__device__ __forceinline__ bool logn_masked(float ln) { return ln * kLog2e == -INFINITY; }
+
+// Partials (m relative to base b) that are joined get the highest base of those with rows that count
+// as their common one B: their m become relative to it. Bases are 0 but beside log-counts far from
+// zero, and a call where all are skips this.
+struct CommonBase {
+  float B = -INFINITY;
+  __device__ __forceinline__ void see(float l, float b) {
+    if (l != 0.f) B = fmaxf(B, b);
+  }
+  __device__ __forceinline__ float settle() {
+    if (B == -INFINITY) B = 0.f;
+    return B;
+  }
+  __device__ __forceinline__ float over(float m, float l, float b) const {
+    return l != 0.f ? m + logn_over(b, B) : m;
+  }
+};
+
 // Cluster kernel: one CTA of 16 warps an SM (all of its clusters have to fit at once).
 constexpr int kPcWarps = 16;
 constexpr int kPcStages = 2;
@@ -125,22 +151,12 @@ __device__ __forceinline__ int unit_span(int L) { return pages_of(L) + kUnitPage
 __device__ __forceinline__ __half2 as_half2(uint32_t u) { return *reinterpret_cast<const __half2*>(&u); }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// A log-count (log2) further than this from what a warp's logits are relative to moves that: its
-// distance to the ones that matter then costs a logit 2^-14 at most.
-constexpr float kFarLogn = 1024.f;
-
-// What the sum s = a + b has lost to rounding, log2 of a factor for the weights whose reference s is.
-// Within 64, so that sums of weights times values stay in fp32; only logits of more than 49 beside
-// log-counts of more than 1.4e9 pass that.
-__device__ __forceinline__ float sum_residual(float a, float b, float s) {
-  return fminf(fmaxf((a - s) + b, -64.f), 64.f);
-}
-
 // One warp's share of a unit: its softmax state over the pages it has taken. load() and prepare()
 // make the unit's operands from its queries (share() and fetch() hand them from one warp to the
 // others), reset() starts a unit, take() adds the first nval rows of a page, end() writes the
-// partial output [G][D] and (m, l) per query head (log2 domain; m is a reference, not always the
-// maximum, and -inf where no row counts).
+// partial output [G][D], (m, l) per query head (log2 domain; m is a reference, not always the
+// maximum, relative to the base of the log-counts, and -inf where no row counts; -l for a base other
+// than 0) and the base.
 
 // fp32: CUDA cores, every product and sum in fp32 (two at a time where they come in pairs), so
 // that it stays within an fp32 softmax attention's own error. Logits with a lane per row, values
@@ -153,9 +169,7 @@ struct PageWarp {
   using P = PageLayout<D>;
   static constexpr int QL = D / 4, RPS = 32 / QL;       // lanes per row of V, rows at a time
   const float (*qs)[D];        // scaled queries, in shared memory
-  // log-counts (log2) are taken relative to `base`, so that logits count beside ones that are far
-  // from zero throughout; so are the maxima
-  float base;
+  float base;                  // of the log-counts; the maxima are relative to it too
   float m[G], l[G];
   float2 acc[G][2];
 
@@ -207,8 +221,8 @@ struct PageWarp {
       for (int g = 0; g < G; ++g) x[g] = fmaf(y[g].x + y[g].y, s, x[g]);
     }
     // rows that count: one whose log-count is -inf does not, whatever it holds
-    const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane)) * kLog2e;
-    const bool counts = lane < nval && ln != -INFINITY;
+    const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane));
+    const bool counts = lane < nval && !logn_masked(ln);
     const uint32_t live = __ballot_sync(0xffffffffu, counts);
     if (__any_sync(0xffffffffu, counts && fabsf(ln - base) > kFarLogn)) {
       const float top = redux_max(counts ? ln : -INFINITY);
@@ -217,14 +231,14 @@ struct PageWarp {
       for (int g = 0; g < G; ++g) none = none && m[g] == -INFINITY;
       if (fabsf(top) < INFINITY && (top - base > kFarLogn || (none && base - top > kFarLogn))) {
 #pragma unroll
-        for (int g = 0; g < G; ++g) m[g] += base - top;
+        for (int g = 0; g < G; ++g) m[g] += logn_over(base, top);
         base = top;
       }
     }
     float p[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float xg = counts ? x[g] + (ln - base) : -INFINITY;
+      const float xg = counts ? x[g] + logn_over(ln, base) : -INFINITY;
       if (__any_sync(0xffffffffu, xg > m[g])) {      // a new maximum: rare after the first pages
         const float M = fmaxf(m[g], warp_max(xg));
         const float f = exp2f(m[g] - M);
@@ -263,17 +277,16 @@ struct PageWarp {
     }
   }
 
-  __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
+  __device__ __forceinline__ void end(float* sa, float* sm, float* sl, float* sb, int lane) {
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-      const float M = base + m[g];
-      const float f = base == 0.f ? 1.f : exp2f(sum_residual(base, m[g], M));
-      const float ls = warp_sum(l[g]) * f;
+      const float ls = warp_sum(l[g]);
       if (lane == 0) {
-        sm[g] = M;
-        sl[g] = ls;
+        sm[g] = m[g];
+        sl[g] = base == 0.f ? ls : -ls;
+        *sb = base;
       }
-      float4 v = make_float4(acc[g][0].x * f, acc[g][0].y * f, acc[g][1].x * f, acc[g][1].y * f);
+      float4 v = make_float4(acc[g][0].x, acc[g][0].y, acc[g][1].x, acc[g][1].y);
       if (RPS == 2) {
         v.x += __shfl_xor_sync(0xffffffffu, v.x, 16);
         v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
@@ -329,8 +342,8 @@ struct PageWarp<bf16, D, G> {
   uint32_t qb[2 * NB][2];      // B of S^T: [2 b + i], k slots (8 t + 2 i, + 4) and (8 t + 2 i + 1, + 5)
   uint32_t cb[2];              // B of the offset: -8 2^-24 sum q' of the blocks, in three half parts
   float f0, f1;                // logit (log2) per unit of the scaled accumulators
-  // The reference of a column (log2) is base - c f: a log-count that the warp's logits are taken
-  // relative to (0 unless log-counts are far from zero), and what the accumulators start from.
+  // The reference of a column (log2) is base log2 e - c f: the base of the log-counts (0 unless they
+  // are far from zero), and what the accumulators start from.
   float base, c0, c1;
   // a logit over the reference by more than this moves it: 15, -inf while there is none
   float lim0, lim1;
@@ -505,12 +518,9 @@ struct PageWarp<bf16, D, G> {
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      // Log-counts may be far from zero (-1e9 for a mask, say): logits are lost against one, but
-      // not against its difference to a base near it. (The products stay rounded; fused into the
-      // differences they would not match the base that came from them.)
       const int r = i * 16 + g;
-      const float na = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e) - base;
-      const float nb = __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r + 8)), kLog2e) - base;
+      const float na = logn_over(*reinterpret_cast<const float*>(pg + P::logn(r)), base);
+      const float nb = logn_over(*reinterpret_cast<const float*>(pg + P::logn(r + 8)), base);
       x[i][0] = fmaf(x[i][0], f0, na);
       x[i][1] = fmaf(x[i][1], f1, na);
       x[i][2] = fmaf(x[i][2], f0, nb);
@@ -600,17 +610,18 @@ struct PageWarp<bf16, D, G> {
   // A row whose log-count is -inf is left out whatever it holds: where keys or values read as NaN,
   // move_reference and scale_values ask for it.
   static __device__ __forceinline__ bool masked(const unsigned char* pg, int r) {
-    return __fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(r)), kLog2e) == -INFINITY;
+    return logn_masked(*reinterpret_cast<const float*>(pg + P::logn(r)));
   }
 
   // Takes the base to the page's largest log-count if that is far above it, or if it is far below
   // and no row has counted yet. The old reference, which the new logits would be lost against, is
   // left in lim (relative to the new base, so far below 0) for move_reference to join with them.
   __device__ __forceinline__ bool move_base(const unsigned char* pg, int lane) {
-    const float top = redux_max(__fmul_rn(*reinterpret_cast<const float*>(pg + P::logn(lane)), kLog2e));
+    const float ln = *reinterpret_cast<const float*>(pg + P::logn(lane));
+    const float top = redux_max(logn_masked(ln) ? -INFINITY : ln);
     if (!(fabsf(top - base) > kFarLogn)) return false;
     if (fabsf(top) == INFINITY || (top < base && __any_sync(0xffffffffu, fmaxf(lim0, lim1) > 0.f))) return false;
-    const float r0 = (base - top) - c0 * f0, r1 = (base - top) - c1 * f1;
+    const float d = logn_over(base, top), r0 = d - c0 * f0, r1 = d - c1 * f1;
     base = top;
     // a reference that logits put so high that it is near the new base, or above it, stays
     c0 = lim0 > 0.f && r0 > -kFarLogn ? -r0 / f0 : 0.f;
@@ -745,20 +756,8 @@ struct PageWarp<bf16, D, G> {
       }
   }
 
-  __device__ __forceinline__ void end(float* sa, float* sm, float* sl, int lane) {
+  __device__ __forceinline__ void end(float* sa, float* sm, float* sl, float* sb, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    const float r0 = -c0 * f0, r1 = -c1 * f1;        // the references are base + r
-    const float m0 = base + r0, m1 = base + r1;
-    if (base != 0.f) {
-      const float e0 = ex2_ftz(sum_residual(base, r0, m0)), e1 = ex2_ftz(sum_residual(base, r1, m1));
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          O[b][j][0] *= e0; O[b][j][1] *= e1; O[b][j][2] *= e0; O[b][j][3] *= e1;
-        }
-      off[0] *= e0; off[1] *= e1;
-    }
     const float l0 = __shfl_sync(0xffffffffu, off[0], 16 + t), l1 = __shfl_sync(0xffffffffu, off[1], 16 + t);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -777,14 +776,15 @@ struct PageWarp<bf16, D, G> {
             make_float4(fmaf(X[1], kUp, -z1), fmaf(X[3] - X[1], kUp / 16, -z1), fmaf(Y[1], kUp, -z1),
                         fmaf(Y[3] - Y[1], kUp / 16, -z1));
     }
+    if (lane == 0) *sb = base;
     if (g == 0) {
       if (2 * t < G) {
-        sm[2 * t] = l0 != 0.f ? m0 : -INFINITY;
-        sl[2 * t] = l0;
+        sm[2 * t] = l0 != 0.f ? -c0 * f0 : -INFINITY;
+        sl[2 * t] = base == 0.f ? l0 : -l0;
       }
       if (2 * t + 1 < G) {
-        sm[2 * t + 1] = l1 != 0.f ? m1 : -INFINITY;
-        sl[2 * t + 1] = l1;
+        sm[2 * t + 1] = l1 != 0.f ? -c1 * f1 : -INFINITY;
+        sl[2 * t + 1] = base == 0.f ? l1 : -l1;
       }
     }
   }
@@ -911,11 +911,12 @@ __device__ __forceinline__ float new_logit(const PageArgs<T>& a, int u, int g, i
   return warp_sum(sp) * (kLog2e / sqrtf((float)D));
 }
 
-// Four columns of an output from the sum A over a unit's rows (weights against M, their sum Ls)
-// and the new row (logit sn, -inf for none).
+// Four columns of an output from the sum A over a unit's rows (weights against M over the base B,
+// their sum Ls) and the new row (logit sn, -inf for none).
 template <typename T>
-__device__ __forceinline__ void finish_columns(float4 A, float M, float Ls, float sn, const T* vn, T* o) {
+__device__ __forceinline__ void finish_columns(float4 A, float M, float Ls, float B, float sn, const T* vn, T* o) {
   if (sn > -INFINITY || sn != sn) {
+    sn += logn_over(0.f, B);
     const float R = fmaxf(M, sn);
     const float fo = Ls != 0.f ? ex2_ftz(M - R) : 0.f, fn = ex2_ftz(sn - R);
     Ls = fmaf(Ls, fo, fn);
@@ -959,22 +960,38 @@ __device__ __forceinline__ void write_new_row(const PageArgs<T>& a, int u, int L
   }
 }
 
-// Sum of the warps' partial outputs, four columns from column c of query head g on.
+// Sum of the warps' partial outputs over their common base B, four columns from column c of query
+// head g on.
 template <int D, int G, int NW>
 __device__ __forceinline__ float4 merge_warps(const float* s_acc, const float (*s_m)[G], const float (*s_l)[G],
-                                              int g, int c, float& M, float& Ls) {
+                                              const float* s_b, int g, int c, float& M, float& Ls, float& B) {
+  uint32_t any = 0u;
   M = -INFINITY;
-  Ls = 0.f;
-#pragma unroll
-  for (int w = 0; w < NW; ++w) M = fmaxf(M, s_m[w][g]);
-  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  Ls = B = 0.f;
 #pragma unroll
   for (int w = 0; w < NW; ++w) {
-    const float f = part_weight(s_m[w][g], s_l[w][g], M);
+    M = fmaxf(M, s_m[w][g]);
+    any |= __float_as_uint(s_l[w][g]);
+  }
+  float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto add = [&](int w, float m) {
+    const float l = fabsf(s_l[w][g]), f = part_weight(m, l, M);
     const float4 v = *reinterpret_cast<const float4*>(s_acc + (w * G + g) * D + c);
     A.x = fmaf(v.x, f, A.x); A.y = fmaf(v.y, f, A.y);
     A.z = fmaf(v.z, f, A.z); A.w = fmaf(v.w, f, A.w);
-    Ls = fmaf(s_l[w][g], f, Ls);
+    Ls = fmaf(l, f, Ls);
+  };
+  if ((int)any >= 0) {
+#pragma unroll
+    for (int w = 0; w < NW; ++w) add(w, s_m[w][g]);
+  } else {
+    CommonBase cb;
+    for (int w = 0; w < NW; ++w) cb.see(s_l[w][g], s_b[w]);
+    B = cb.settle();
+    M = -INFINITY;
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, cb.over(s_m[w][g], s_l[w][g], s_b[w]));
+#pragma unroll 1
+    for (int w = 0; w < NW; ++w) add(w, cb.over(s_m[w][g], s_l[w][g], s_b[w]));
   }
   return A;
 }
@@ -989,7 +1006,8 @@ page_decode_kernel(const PageArgs<T> a) {
   float* s_acc = reinterpret_cast<float*>(dsm + S::kRing);                  // [NW][G][D]
   __shared__ __align__(16) unsigned char s_q[PageWarp<T, D, G>::kShare];    // a unit's operands
   __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
-  __shared__ float s_m[NW][G], s_l[NW][G], s_stat[G][2];
+  __shared__ float s_m[NW][G], s_l[NW][G], s_stat[G][3];
+  __shared__ float s_b[NW];
   __shared__ float s_new[3][G];   // the new row's logits, for the units of s_split and a whole one
   __shared__ int s_len[kPdLens];  // lengths (as they are in memory) of units from the first one on
   // the unit that began in an earlier CTA (0) and the one that goes on in a later one (1): unit,
@@ -1177,7 +1195,7 @@ page_decode_kernel(const PageArgs<T> a) {
       if (more || seg != f0) __syncthreads();      // the last unit's partials, this one's operands: read
       const int len = len_of(u);
       const int id = nsplit == 1 ? new_row(u, len, 2) : -1;
-      pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
+      pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], s_b + warp, lane);
       if (more && first_warp) {
         pw.prepare(lane);
         pw.share(s_q, lane);
@@ -1185,16 +1203,16 @@ page_decode_kernel(const PageArgs<T> a) {
       __syncthreads();
       if (tid < G * D / 4) {
         const int g = tid * 4 / D, c = tid * 4 % D;
-        float M, Ls;
-        const float4 A = merge_warps<D, G, NW>(s_acc, s_m, s_l, g, c, M, Ls);
+        float M, Ls, B;
+        const float4 A = merge_warps<D, G, NW>(s_acc, s_m, s_l, s_b, g, c, M, Ls, B);
         if (nsplit == 1) {
-          finish_columns<T>(A, M, Ls, id >= 0 ? s_new[2][g] : -INFINITY, a.v_new + (size_t)u * D + c,
+          finish_columns<T>(A, M, Ls, B, id >= 0 ? s_new[2][g] : -INFINITY, a.v_new + (size_t)u * D + c,
                             a.out + (size_t)u * G * D + tid * 4);
         } else {
           // a row of the workspace; who finishes the unit is settled after this CTA's last page
           float* row = a.part + ((size_t)blockIdx.x * 2 + slot) * G * RS + g * RS;
           *reinterpret_cast<float4*>(row + c) = A;
-          if (c == 0) *reinterpret_cast<float2*>(row + D) = make_float2(M, Ls);
+          if (c == 0) *reinterpret_cast<float4*>(row + D) = make_float4(M, Ls, B, 0.f);
         }
       }
       if (nsplit == 1)
@@ -1235,18 +1253,28 @@ page_decode_kernel(const PageArgs<T> a) {
         // few splits (the usual case): every thread weighs them for itself, one round trip
         if (tid < NU) {
           const int g = tid * 4 / D, c = tid * 4 % D;
-          float2 ml[kFew];
-          float4 v[kFew];
+          float4 ml[kFew], v[kFew];
+          uint32_t any = 0u;
 #pragma unroll
           for (int s = 0; s < kFew; ++s) {
-            ml[s] = make_float2(-INFINITY, 0.f);
+            ml[s] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
             v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
             if (s < np) {
-              ml[s] = __ldcg(reinterpret_cast<const float2*>(row_of(s) + g * RS + D));
+              ml[s] = __ldcg(reinterpret_cast<const float4*>(row_of(s) + g * RS + D));
               v[s] = __ldcg(reinterpret_cast<const float4*>(row_of(s) + g * RS + c));
             }
           }
-          float M = -INFINITY, Ls = 0.f;
+          float M = -INFINITY, Ls = 0.f, B = 0.f;
+#pragma unroll
+          for (int s = 0; s < kFew; ++s) any |= __float_as_uint(ml[s].z);
+          if (any != 0u) {
+            CommonBase cb;
+#pragma unroll
+            for (int s = 0; s < kFew; ++s) cb.see(ml[s].y, ml[s].z);
+            B = cb.settle();
+#pragma unroll
+            for (int s = 0; s < kFew; ++s) ml[s].x = cb.over(ml[s].x, ml[s].y, ml[s].z);
+          }
 #pragma unroll
           for (int s = 0; s < kFew; ++s) M = fmaxf(M, ml[s].x);
           float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1257,7 +1285,7 @@ page_decode_kernel(const PageArgs<T> a) {
             A.x = fmaf(v[s].x, f, A.x); A.y = fmaf(v[s].y, f, A.y);
             A.z = fmaf(v[s].z, f, A.z); A.w = fmaf(v[s].w, f, A.w);
           }
-          finish_columns<T>(A, M, Ls, id >= 0 ? s_new[i][g] : -INFINITY, a.v_new + (size_t)u * D + c,
+          finish_columns<T>(A, M, Ls, B, id >= 0 ? s_new[i][g] : -INFINITY, a.v_new + (size_t)u * D + c,
                             a.out + (size_t)u * G * D + tid * 4);
         }
         append(u, sp.w, id);
@@ -1275,16 +1303,28 @@ page_decode_kernel(const PageArgs<T> a) {
       load_batch(grp);                             // with the factors' loads: one round trip for both
       if (warp < G) {
         constexpr int kPer = (kPageDecodeCtas + 31) / 32;
-        float2 ml[kPer];
-        float M = -INFINITY, Ls = 0.f;
+        float4 ml[kPer];
+        float M = -INFINITY, Ls = 0.f, B = 0.f;
+        uint32_t any = 0u;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const int s = lane + j * 32;
-          ml[j] = make_float2(-INFINITY, 0.f);
+          ml[j] = make_float4(-INFINITY, 0.f, 0.f, 0.f);
           if (j * 32 < np && s < np)
-            ml[j] = __ldcg(reinterpret_cast<const float2*>(row_of(s) + warp * RS + D));
-          M = fmaxf(M, ml[j].x);
+            ml[j] = __ldcg(reinterpret_cast<const float4*>(row_of(s) + warp * RS + D));
+          any |= __float_as_uint(ml[j].z);
         }
+        if (__any_sync(0xffffffffu, any != 0u)) {
+          CommonBase cb;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) cb.see(ml[j].y, ml[j].z);
+          cb.B = warp_max(cb.B);
+          B = cb.settle();
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) ml[j].x = cb.over(ml[j].x, ml[j].y, ml[j].z);
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) M = fmaxf(M, ml[j].x);
         M = warp_max(M);
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
@@ -1297,6 +1337,7 @@ page_decode_kernel(const PageArgs<T> a) {
         if (lane == 0) {
           s_stat[warp][0] = M;
           s_stat[warp][1] = Ls;
+          s_stat[warp][2] = B;
         }
       }
       __syncthreads();
@@ -1323,7 +1364,7 @@ page_decode_kernel(const PageArgs<T> a) {
           }
       }
       if (grp == 0) {
-        finish_columns<T>(A, s_stat[g][0], s_stat[g][1], id >= 0 ? s_new[i][g] : -INFINITY,
+        finish_columns<T>(A, s_stat[g][0], s_stat[g][1], s_stat[g][2], id >= 0 ? s_new[i][g] : -INFINITY,
                           a.v_new + (size_t)u * D + c, a.out + (size_t)u * G * D + unit * 4);
       }
       append(u, sp.w, id);
@@ -1337,9 +1378,18 @@ page_decode_kernel(const PageArgs<T> a) {
   }
 }
 
-// Weighs the partials (m, l, A) of the 16 lanes of a half-warp and sums them up in every lane (A,
-// l); returns the reference.
-__device__ __forceinline__ float half_warp_sum(float4& A, float m, float& l) {
+// Weighs the partials (m over base b, l, A) of the 16 lanes of a half-warp and sums them up in every
+// lane (A, l, the common base b); returns the reference.
+__device__ __forceinline__ float half_warp_sum(float4& A, float m, float& l, float& b) {
+  if (__any_sync(0xffffffffu, b != 0.f)) {
+    CommonBase cb;
+    cb.see(l, b);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) cb.B = fmaxf(cb.B, __shfl_xor_sync(0xffffffffu, cb.B, o));
+    cb.settle();
+    m = cb.over(m, l, b);
+    b = cb.B;
+  }
   float M = m;
 #pragma unroll
   for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -1378,7 +1428,8 @@ page_decode_cluster_kernel(const PageArgs<T> a, int clusters) {
   __shared__ __align__(16) float s_q[sizeof(T) == 4 ? G * D : 4];           // fp32: PageWarp::share
   __shared__ __align__(16) __half s_ones[NW][16];                           // bf16: PageWarp::init
   __shared__ float s_m[NW][G], s_l[NW][G], s_new[G];
-  __shared__ __align__(8) float s_ml[G][2];                                 // read by peers
+  __shared__ float s_b[NW];
+  __shared__ __align__(16) float s_ml[G][4];                                // (m, l, base), read by peers
 
   griddep_wait();                 // launched with programmatic stream serialisation
   griddep_launch_dependents();
@@ -1420,15 +1471,14 @@ page_decode_cluster_kernel(const PageArgs<T> a, int clusters) {
   if (!pr.run((pages_of(L) - first + step * (NW - warp) - 1) / (step * NW), lane, [] { return 0u; },
               [&](unsigned char* pg, int n) { pw.take(pg, n, lane); }))
     set_flag(a.flags, KVS_FLAG_TIMEOUT);
-  pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], lane);
+  pw.end(s_acc + warp * G * D, s_m[warp], s_l[warp], s_b + warp, lane);
   __syncthreads();
   for (int i = tid; i < G * D / 4; i += NW * 32) {
     const int g = i * 4 / D, c = i * 4 % D;
-    float M, Ls;
-    *reinterpret_cast<float4*>(s_sum + i * 4) = merge_warps<D, G, NW>(s_acc, s_m, s_l, g, c, M, Ls);
+    float M, Ls, B;
+    *reinterpret_cast<float4*>(s_sum + i * 4) = merge_warps<D, G, NW>(s_acc, s_m, s_l, s_b, g, c, M, Ls, B);
     if (c == 0) {
-      s_ml[g][0] = M;
-      s_ml[g][1] = Ls;
+      *reinterpret_cast<float4*>(s_ml[g]) = make_float4(M, Ls, B, 0.f);
     }
   }
   cluster_arrive();
@@ -1439,23 +1489,24 @@ page_decode_cluster_kernel(const PageArgs<T> a, int clusters) {
   for (int b0 = lo + 2 * warp; b0 < hi; b0 += 2 * NW) {
     const int b = b0 + (lane >> 4), src = lane & 15;
     const int g = min(b, NU - 1) * 4 / D, c = b * 4 % D;
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, base = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
     if (b < hi && src < C) {
-      const float2 ml = ld_cluster_f32x2(cluster_map(smem_u32(&s_ml[g][0]), src));
+      const float4 ml = ld_cluster_f32x4(cluster_map(smem_u32(&s_ml[g][0]), src));
       A = ld_cluster_f32x4(cluster_map(smem_u32(s_sum + b * 4), src));
       m = ml.x;
       l = ml.y;
+      base = ml.z;
     }
-    const float M = half_warp_sum(A, m, l);
+    const float M = half_warp_sum(A, m, l, base);
     if (b < hi && src == 0) {
       if (clusters == 1) {
-        finish_columns<T>(A, M, l, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
+        finish_columns<T>(A, M, l, base, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
                           a.out + (size_t)u * G * D + b * 4);
       } else {
         float* row = a.part + (((size_t)u * clusters + part) * NU + b) * 8;
         *reinterpret_cast<float4*>(row) = A;
-        *reinterpret_cast<float2*>(row + 4) = make_float2(M, l);
+        *reinterpret_cast<float4*>(row + 4) = make_float4(M, l, base, 0.f);
       }
     }
   }
@@ -1471,18 +1522,19 @@ page_decode_cluster_kernel(const PageArgs<T> a, int clusters) {
       for (int b0 = lo + 2 * warp; b0 < hi; b0 += 2 * NW) {
         const int b = b0 + (lane >> 4), src = lane & 15;
         const int g = min(b, NU - 1) * 4 / D, c = b * 4 % D;
-        float m = -INFINITY, l = 0.f;
+        float m = -INFINITY, l = 0.f, base = 0.f;
         float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
         if (b < hi && src < clusters) {
           const float* row = a.part + (((size_t)u * clusters + src) * NU + b) * 8;
           A = __ldcg(reinterpret_cast<const float4*>(row));
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(row + 4));
+          const float4 ml = __ldcg(reinterpret_cast<const float4*>(row + 4));
           m = ml.x;
           l = ml.y;
+          base = ml.z;
         }
-        const float M = half_warp_sum(A, m, l);
+        const float M = half_warp_sum(A, m, l, base);
         if (b < hi && src == 0)
-          finish_columns<T>(A, M, l, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
+          finish_columns<T>(A, M, l, base, new_id >= 0 ? s_new[g] : -INFINITY, a.v_new + (size_t)u * D + c,
                             a.out + (size_t)u * G * D + b * 4);
       }
       if (tid == 0) a.counters[u * C + rank] = 0;

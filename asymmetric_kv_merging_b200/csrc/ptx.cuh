@@ -342,16 +342,11 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t addr, float4 v) {
                : "memory");
 }
 
-// Loads from the shared memory of a CTA of the cluster (shared::cluster address).
+// Load from the shared memory of a CTA of the cluster (shared::cluster address).
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
-__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
-  float2 v;
-  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
 }
 

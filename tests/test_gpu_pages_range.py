@@ -240,3 +240,35 @@ def test_fp32_logits_count_beside_a_far_log_count_that_all_rows_have(kvs, shape,
     c.store()
     q = c.queries(4.0)
     c.check(q, c.decode(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [-3e5, 2e4, -5e6])
+def test_far_log_counts_that_differ(kvs, dtype, shape, low):
+    """Counts of 1 to 20 beside a common offset: their differences are exact in fp32 and count."""
+    units, wide = shape
+    c = Units(kvs, units, 4096, 2, 64, dtype, seed=8, wide=wide)
+    n = torch.randint(1, 21, c.logn.shape, generator=c.gen, device=DEV)
+    c.logn[:] = low + torch.log(n.float())
+    c.store()
+    q = c.queries(1.0)
+    c.check(q, c.decode(q))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("low", [0.0, -1e9, -1e30, 1e30])
+def test_large_logits_beside_far_log_counts(kvs, dtype, shape, low):
+    """Logits of up to about 80, with masked rows in between and a row appended."""
+    units, wide = shape
+    c = Units(kvs, units, 4096, 2, 64, dtype, seed=9, wide=wide)
+    c.logn[:] = low
+    c.logn[:, :, torch.arange(4096, device=DEV) // 64 % 3 == 1] = -2e30
+    c.store()
+    q = c.queries(18.0)
+    c.check(q, c.decode(q))
+    kn, vn = c.randn(1, units, 64).to(dtype), c.randn(1, units, 64).to(dtype)
+    out = c.decode(q, kn, vn)
+    if low < 0:                                              # nothing but the new row
+        assert torch.equal(out.view(units, 2, 64), vn[0, :, None].expand(-1, 2, -1))
+    elif low > 0:                                            # everything but it
+        c.check(q, out)
