@@ -18,13 +18,13 @@
 //
 // Measured on one B200 (G = 4, d = 128, bf16; device time of captured back-to-back launches over
 // three caches in turn, so that pages come from L2 up to 8 x 16384 rows; bytes are 148 a row):
-//   cluster   8 units x  2048 rows    6.6 us (2.4 MB: launch, three round trips and the combine)
-//             8 units x 16384 rows   11.3 us, 1.7 TB/s
-//             8 units x 32768 rows   16.9 us, 2.3 TB/s (80 SMs: ten CTAs are the largest cluster
+//   cluster   8 units x  2048 rows    6.8 us (2.4 MB: launch, three round trips and the combine)
+//             8 units x 16384 rows   11.7 us, 1.7 TB/s
+//             8 units x 32768 rows   17.1 us, 2.3 TB/s (80 SMs: ten CTAs are the largest cluster
 //                                    of which eight fit the GPU at once)
-//             1 unit x 131072 rows   12.8 us (8 clusters), 1.5 TB/s
+//             1 unit x 131072 rows   13.2 us (8 clusters), 1.5 TB/s
 //   split    64 units x 11K..22K     39.0 us, 4.0 TB/s = 0.61 of the measured copy peak
-//           128 units x 1K..8K       30.0 us, 2.9 TB/s
+//           128 units x 1K..8K       29.9 us, 2.9 TB/s
 // The same kernels without the arithmetic take 4.1, 5.7, 10.2 us for 8 units, 31.5 and 23.1 us: the
 // split kernel is bound first by how it brings the pages in (the lengths, the numbering and the page
 // numbers before the first of them; barriers of all warps at the end of every unit; the ends), and
@@ -110,9 +110,9 @@ struct PageClusterShape {
 // A cluster per unit, or the split kernel? The cluster's launch costs 4 to 5 us less (no numbering,
 // no round trip to the workspace), but the longest unit sets its time, and the host knows only
 // how many pages a unit may have. Measured (us, G = 4, d = 128, equal lengths; cluster | split):
-//   8 units (C = 10)   2048 rows  6.6 | 10.8   16384 rows 11.3 | 13.8   65536 rows 26.7 | 25.4
-//   32 units (C = 4)   2048 rows  7.4 | 11.5   16384 rows 20.0 | 24.6
-//   64 units (C = 2)    512 rows  7.3 | 10.2    8192 rows 20.5 | 24.6
+//   8 units (C = 10)   2048 rows  6.8 | 10.9   16384 rows 11.7 | 14.0   65536 rows 26.9 | 25.5
+//   32 units (C = 4)   2048 rows  7.8 | 11.6   16384 rows 20.1 | 24.7
+//   64 units (C = 2)    512 rows  7.3 | 10.4    8192 rows 20.5 | 24.7
 // A lone full unit of 64 C pages among empty ones takes the cluster 12 us and the split kernel 9 to
 // 12; one of 128 C pages 18 us, a risk that is taken for the few units that C >= 8 means, as they are
 // mostly the heads of one sequence.
@@ -124,9 +124,9 @@ static bool use_cluster(int C, int clusters, int max_pages) {
 
 // Clusters of a unit: one or two units with wide tables have 8 in all. A cluster has at most 16
 // CTAs, and 8 clusters of 10 run side by side. Measured (us, G = 4, d = 128; several clusters | what
-// it would be else): one unit with a table of 1025 pages 8.8 | 11.5 at 32768 rows, 8.0 | 5.9 at 2048;
-// with 4097 pages (else the split kernel) 12.8 | 26.4 at 131072 rows, 7.9 | 9.4 at 2048; two units of
-// 4097 pages 18.5 | 25.9 and 7.9 | 9.6. With 513 pages it is 7.9 | 8.2 when they are full and
+// it would be else): one unit with a table of 1025 pages 9.1 | 12.1 at 32768 rows, 8.1 | 6.2 at 2048;
+// with 4097 pages (else the split kernel) 13.2 | 26.6 at 131072 rows, 8.1 | 9.4 at 2048; two units of
+// 4097 pages 18.5 | 25.7 and 8.1 | 9.8. With 513 pages it is 7.9 | 8.2 when they are full and
 // 7.6 | 5.6 at 2048 rows, and four units of 1025 pages lose (12.5 | 11.7): the workspace's round
 // trip costs 1.6 us. The table's width decides, not a length: a unit's CTAs could read different
 // lengths once one of them has appended.
@@ -138,7 +138,7 @@ static int clusters_of(int units, int max_pages) {
 
 // How many pages more than the mean the longest unit may have in a CTA for a split by units.
 // Measured (us, equal lengths; by units | even runs): 16 units x 8192 rows 12.5 | 15.4, 128 x 2048
-// 17.7 | 19.9, 256 x 512 11.8 | 17.1, 64 x 16384 38.9 | 38.1; on the ragged batches of 64 and 128
+// 17.8 | 20.0, 256 x 512 11.9 | 17.1, 64 x 16384 39.0 | 38.0; on the ragged batches of 64 and 128
 // units, which the rule leaves to the even runs, 45.7 | 38.3 and 37.3 | 29.2.
 constexpr int kByUnit = 40;
 
@@ -323,16 +323,17 @@ struct PageWarp {
 // scale_values (with scales taken as they are, those of 2^-17 lost a third of their range, and
 // what a row lost of u w stayed in 8 scale p).
 //
-// What bounds it: 456 instructions a page (32 rows, d = 128), of which 214 on the integer pipe,
+// What bounds it: 462 instructions a page (32 rows, d = 128), of which 207 on the integer pipe,
 // which takes one every other cycle, and 36 MMAs of 8 cycles on the tensor pipe of the legacy
 // MMAs; the two hardly overlap. About 197 cycles a page and SM, from 12 warps an SM on (20 warps
 // at 96 registers gain nothing), where an SM's share of the copy peak brings a page in 203: both
 // bounds at once. Converting the codes to half instead costs 8 conversions and 8 products a word
 // where this takes 4 or 5 integer operations; unpacking for tcgen05 would have to write every
 // unpacked register to tensor memory first. Fragments by ldmatrix instead of 27 more loads and the
-// weight sums by MMA took the page from 507 to 456. The reference in two parts and the units of the
-// V scales cost a page nothing, but the first page of a warp 0.3 us; with the scales of every page
-// out of range 64 units take 44 (values of 1e-4) to 46 us (of 30).
+// weight sums by MMA took the page from 507 to 450. The reference in two parts, the units of the V
+// scales and the bases of the partials cost 0.5 us a launch, nearly all of it at the first page of a
+// warp and at the end of a unit; with the scales of every page out of range 64 units take 8% (values
+// of 1e-4) to 16% longer (of 30).
 
 template <int D, int G>
 struct PageWarp<bf16, D, G> {
