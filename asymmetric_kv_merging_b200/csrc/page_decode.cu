@@ -11,8 +11,8 @@
 //    itself. The pages of all units (KV heads of all sequences) are numbered one unit after
 //    another and dealt out in even runs, or a fixed number of CTAs goes to each unit. A unit that
 //    lies in one CTA is finished there; one that spans several gets a partial row per CTA in the
-//    workspace, and the last of them to arrive (a counter at the first of them) combines. No CTA waits for
-//    another.
+//    workspace, and the last of them to arrive (a counter at the first of them) combines. No CTA
+//    waits for another.
 //  - cluster kernel: one thread-block cluster per unit, combined in distributed shared memory (one
 //    or two units with wide tables: several, joined through the workspace).
 //

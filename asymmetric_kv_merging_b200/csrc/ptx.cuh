@@ -459,7 +459,7 @@ __device__ __forceinline__ float max3_nan(float a, float b, float c) {
 // Maximum over a warp (sm_100; NaN is ignored).
 __device__ __forceinline__ float redux_max(float a) {
   float d;
-  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(a));
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(a));
   return d;
 }
 

@@ -19,6 +19,7 @@ row with a weight has:
 """
 
 import gc
+import random
 
 import pytest
 import torch
@@ -69,7 +70,8 @@ class Units:
         self.ws = kvs.workspace(self.desc, ops=(kvs.OP_PAGES,))
         kvs.page_store(f32, self.K, self.V, self.logn, slots, self.pool, self.ws)
         kvs.page_load(f32, self.pool, slots, self.K, self.V, None, self.ws)
-        self.lens = torch.full((units,), T, dtype=torch.int32, device=DEV)
+        if not hasattr(self, "lens"):
+            self.lens = torch.full((units,), T, dtype=torch.int32, device=DEV)
         return self
 
     def queries(self, scale):
@@ -87,12 +89,22 @@ class Units:
         s = self.pages[at, 34 * self.d:36 * self.d].view(torch.float16).view(len(at), -1, PAGE)
         return s.transpose(1, 2).reshape(-1, self.d // 32)[:self.T].double()
 
-    def check(self, q, out, extra=0.0, but=None):
-        """`extra`: what log-counts of rows without a weight add to X. `but`: a unit to leave out."""
-        d, T, worst = self.d, self.T, 0.0
+    def check(self, q, out, extra=0.0, but=None, lens=None, new=None):
+        """`extra`: what log-counts of rows without a weight add to X. `but`: a unit to leave out.
+        `lens`: rows of each unit, if not T. `new`: keys and values [units, d] of a row appended."""
+        d, worst = self.d, 0.0
         q, out = (x.view(self.units, self.G, d).double() for x in (q, out))
         for u in [u for u in range(self.units) if u != but]:
-            k, v, ln = self.K[0, u].double(), self.V[0, u].double(), self.logn[0, u].double()
+            T = self.T if lens is None else lens[u]
+            keep = self.logn[0, u, :T] * 1.44269504 > -float("inf")
+            k, v, ln = (x[0, u, :T][keep].double() for x in (self.K, self.V, self.logn))
+            s = self.scales(u)[:T][keep].repeat_interleave(32, 1)
+            if new is not None:
+                k, v = (torch.cat([x, y[u, None].double()]) for x, y in zip((k, v), new))
+                ln, s = torch.cat([ln, ln.new_zeros(1)]), torch.cat([s, s.new_zeros(1, d)])
+            if len(k) == 0:
+                assert not out[u].any()
+                continue
             ln = ln - ln.max()                               # the same softmax, and exact
             w = torch.softmax(q[u] @ k.T / d ** 0.5 + ln, -1)
             want, size = w @ v, w @ v.abs()
@@ -101,7 +113,6 @@ class Units:
             bound = (2 * (d + 6) * 2.0 ** -24 * x + (T + 16) * 2.0 ** -24 + 2.0 ** -21) * size
             bound += 2.0 ** -24 * want.abs()
             if self.dtype == torch.bfloat16:
-                s = torch.where(live[:, None], self.scales(u).repeat_interleave(32, 1), 0)
                 top = s.max(0).values
                 unit = torch.where((top >= 2.0 ** -6) & (top < 1), 1.0, 2 * top)
                 bound += 2.0 ** -11 * (size + want.abs()) + 15 * 2.0 ** -11 * (w @ s) + 2.0 ** -8 * want.abs()
@@ -272,3 +283,34 @@ def test_large_logits_beside_far_log_counts(kvs, dtype, shape, low):
         assert torch.equal(out.view(units, 2, 64), vn[0, :, None].expand(-1, 2, -1))
     elif low > 0:                                            # everything but it
         c.check(q, out)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("seed", range(12))
+def test_everything_at_once(kvs, dtype, seed):
+    """Ragged units, values of a size of their own in every block, far log-counts, masks of several
+    kinds with NaN where nothing counts, and a row appended."""
+    rng = random.Random(seed)
+    units, wide = rng.choice([(1, 1100), (2, 0), (8, 0), (8, 6000), (64, 0), (150, 1100), (310, 0)])
+    G, d, T = rng.choice([1, 2, 4, 8]), rng.choice([64, 128]), 2 * rng.randint(1, 300000 // units // 2 // 15)
+    c = Units(kvs, units, T, G, d, dtype, seed, wide=wide)
+    gen, t = c.gen, torch.arange(T, device=DEV)
+    for b in range(0, d, 32):
+        c.V[..., b:b + 32] *= 10.0 ** rng.uniform(-7, 4.5)
+    c.logn[:] = rng.choice([0, 0, -3e5, -1e9, 2e4]) + torch.rand(c.logn.shape, generator=gen, device=DEV)
+    for low in rng.sample([-1e4, -1e9, -1e30, -float("inf"), torch.finfo(torch.float32).min], 2):
+        off = {"pages": torch.rand(units, T // PAGE + 1, generator=gen, device=DEV).repeat_interleave(PAGE, 1)[:, :T] < .6,
+               "rows": torch.rand(units, T, generator=gen, device=DEV) < .5, "head": (t < T // 2).expand(units, T),
+               "units": (torch.rand(units, 1, generator=gen, device=DEV) < .3).expand(units, T)}
+        c.logn[0][off[rng.choice(list(off))]] = low
+    gone = c.logn[0] * 1.44269504 == -float("inf")
+    c.K[0][gone & (torch.rand(units, T, generator=gen, device=DEV) < .3)] = float("nan")
+    c.V[0][gone & (torch.rand(units, T, generator=gen, device=DEV) < .3)] = float("inf")
+    c.lens = torch.randint(0, T + 1, (units,), generator=gen, device=DEV).to(torch.int32)
+    lens = c.lens.tolist()
+    c.store()
+    q = c.queries(rng.choice([0.3, 2.0, 8.0]))
+    c.check(q, c.decode(q), lens=lens)
+    new = [c.randn(units, d).to(dtype) for _ in range(2)]
+    c.check(q, c.decode(q, *new), lens=lens, new=new)
+    assert c.lens.tolist() == [n + 1 for n in lens]
